@@ -9,6 +9,11 @@
  *      tokens: device absmax (fp8_kv_amax_observe), staging of the window's
  *      bf16 K/V, the freeze and the chronological replay
  *      (fp8_kv_calib_* and fp8_kv_freeze_replay).
+ * And the attention layer's step around a paged cache of half that size:
+ *   4. K and V quantised to 4 bits as they are written to the cache, read back,
+ *      and attended to (fp4_kv_write, fp4_kv_read, fp4_kv_attention);
+ *   5. the norms of queries and keys with the position rotation
+ *      (qk_norm_rope).
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -63,6 +68,8 @@ typedef int32_t fp8q_status;
 /* Bits of the sticky per-device error word. */
 #define FP8Q_DEVERR_SLOT_OUT_OF_RANGE 0x1u  /* slot >= num_blocks*block_size: token skipped */
 #define FP8Q_DEVERR_BAD_SCALE 0x2u          /* device scale NaN or <= 0: tensor not written */
+#define FP8Q_DEVERR_BAD_SEQUENCE 0x4u       /* sequence length or query range outside its buffers: cut */
+#define FP8Q_DEVERR_WAIT 0x8u               /* a copy did not arrive in time: output not valid */
 
 /* E4M3 saturation value and the group width of the activation quantizer. */
 #define FP8Q_E4M3_MAX 448.0f
@@ -531,6 +538,195 @@ FP8Q_API fp8q_status fp8_kv_calib_window_noalloc(
  * its window (also for n == 0), else 0; -1 if states is NULL with n > 0.
  */
 FP8Q_API int32_t fp8_kv_graphs_ready(const int8_t *states, int64_t n);
+
+/* ------------------------------------------------------------------------ */
+/* 4. A paged KV cache held in 4 bits                                       */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * The cache.  A value is E2M1 code * E4M3 block scale * fp32 tensor scale: a
+ * block is 16 neighbouring dimensions of one token's head, and k_scale or
+ * v_scale holds for the whole pool.  An E2M1 code is four bits, the sign and
+ * then 0, .5, 1, 1.5, 2, 3, 4, 6.  A token's head takes 9/16 byte a dimension.
+ *
+ * A pool is num_blocks blocks of block_size slots, block_stride bytes apart.
+ * A block is [num_kv_heads][block_size / 16] tiles of 9 * head_dim bytes.  A
+ * tile holds 16 consecutive slots of one head: 8 * head_dim bytes of codes
+ * (two to a byte, the even dimension in the low half), then head_dim bytes of
+ * block scales.  K tiles are token-major, V tiles block-major:
+ *   K codes [16][head_dim / 2]          K scales [16][head_dim / 16]
+ *   V codes [head_dim / 16][16][8]      V scales [head_dim / 16][16]
+ *
+ * Common arguments
+ *   num_kv_heads  > 0; head_dim 64, 128 or 256
+ *   k_pool,
+ *   v_pool        device pools, 16-byte aligned, num_blocks * block_stride
+ *                 bytes each
+ *   block_size    slots of a block, a positive multiple of 16
+ *   block_stride  BYTES between blocks, a multiple of 16, at least
+ *                 num_kv_heads * block_size / 16 * 9 * head_dim
+ *   num_blocks    >= 0
+ *   k_scale,
+ *   v_scale       in [2^-96, 2^96]; used when scale_dev is NULL
+ *   scale_dev     NULL, or device fp32 [2] = {k_scale, v_scale}, 8-byte
+ *                 aligned; a value outside that range sets
+ *                 FP8Q_DEVERR_BAD_SCALE and its tensor (for attention: every
+ *                 output) is left unwritten
+ */
+
+/*
+ * fp4_kv_write -- quantise K and V to 4 bits and scatter them into the pools.
+ *
+ * The 4-bit counterpart of fp8_kv_write, with its slot rules: a negative slot
+ * is skipped, one past the pool is skipped and sets
+ * FP8Q_DEVERR_SLOT_OUT_OF_RANGE, and two tokens of one call must not share a
+ * slot.  For a block x[0..15] of a token's head, s the tensor's scale, every
+ * step rounded to fp32:
+ *   b    = E4M3(max|x| / 6 / s)          to nearest-even, at most 448
+ *   r    = 1 / (b * s), or 0 where b * s is 0
+ *   code = E2M1(x * r)                   to nearest-even, at most 6, the sign
+ *                                        of zero kept
+ * No input leaves a NaN in the cache: infinities saturate, and a NaN counts as
+ * nothing in max|x| and is stored as the largest code.
+ *
+ *   k, v          device bf16 [num_tokens, num_kv_heads, head_dim] rows;
+ *                 16-byte aligned
+ *   key_stride,
+ *   value_stride  elements between token rows; >= num_kv_heads * head_dim,
+ *                 multiples of 8
+ *   slot_mapping  device int64 [num_tokens]
+ *   num_tokens    >= 0; 0 is a no-op
+ * Returns FP8Q_OK, FP8Q_EINVAL, FP8Q_ECUDA.
+ */
+FP8Q_API fp8q_status fp4_kv_write(const void *k, const void *v, int64_t key_stride,
+                                  int64_t value_stride, const int64_t *slot_mapping,
+                                  int64_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                                  void *k_pool, void *v_pool, int32_t block_size,
+                                  int64_t block_stride, int64_t num_blocks, float k_scale,
+                                  float v_scale, const float *scale_dev, void *stream);
+
+/*
+ * fp4_kv_read -- gather cached tokens back as bf16 rows.
+ *
+ * For each token t with slot = slot_mapping[t], the value
+ * bf16(fp32(code * block scale * tensor scale)) of every element; code * block
+ * scale is exact.  Rows of negative slots are left as they were, so are those
+ * of slots past the pool (FP8Q_DEVERR_SLOT_OUT_OF_RANGE).  A slot may be read
+ * any number of times.
+ *
+ *   k, v          device bf16 rows to write, as for fp4_kv_write
+ * Returns FP8Q_OK, FP8Q_EINVAL, FP8Q_ECUDA.
+ */
+FP8Q_API fp8q_status fp4_kv_read(void *k, void *v, int64_t key_stride, int64_t value_stride,
+                                 const int64_t *slot_mapping, int64_t num_tokens,
+                                 int32_t num_kv_heads, int32_t head_dim, const void *k_pool,
+                                 const void *v_pool, int32_t block_size, int64_t block_stride,
+                                 int64_t num_blocks, float k_scale, float v_scale,
+                                 const float *scale_dev, void *stream);
+
+/*
+ * fp4_kv_attention -- causal attention of new tokens over the 4-bit cache.
+ *
+ * Sequence b has seq_lens[b] cached tokens; token j of it lies in slot
+ * j % block_size of block block_table[b][j / block_size].  Its n new tokens
+ * are rows q_start[b] .. q_start[b + 1] - 1 of q (q_start NULL: row b alone)
+ * and are the last n of the cached ones: write them first.  New token i sees
+ * the tokens j <= p = seq_lens[b] - n + i, with a window only those with
+ * j > p - window.  Query head h reads KV head h / (num_q_heads / num_kv_heads).
+ *   out = softmax_j(softmax_scale * q.k_j) v_j,
+ *   lse = log sum_j exp(softmax_scale * q.k_j)
+ * A row that sees no token gets out = 0 and lse = -infinity.  Rows of q that no
+ * sequence has keep what out and lse held.  Scores, sums and outputs are fp32,
+ * rounded once to bf16; the softmax weights are rounded to fp16 for the second
+ * product.  The result does not depend on what unused slots hold, and is the
+ * same in every run on one kind of GPU.
+ *
+ * The lengths and tables are read on the device, and the launches depend on
+ * the sizes alone: a captured call may be replayed with other contents.  A
+ * length below 0 or past the table and a query range outside the rows are cut
+ * to what is there (FP8Q_DEVERR_BAD_SEQUENCE); for a block outside the pool
+ * block 0 is read (FP8Q_DEVERR_SLOT_OUT_OF_RANGE).  Entries of block_table
+ * that hold no seen token are not looked at.
+ *
+ *   q             device bf16 [num_tokens, num_q_heads, head_dim] rows, 16-byte
+ *                 aligned; q_stride elements between rows, a multiple of 8
+ *   block_table   device int32 [batch, table_width], table_stride elements
+ *                 between rows; table_width * block_size <= 2^30
+ *   seq_lens      device int32 [batch]
+ *   q_start       device int32 [batch + 1], not decreasing, or NULL, which
+ *                 needs num_tokens == batch
+ *   batch,
+ *   num_tokens    >= 0; 0 is a no-op; num_tokens * num_q_heads <= 2^30
+ *   num_q_heads   a positive multiple of num_kv_heads
+ *   softmax_scale finite, > 0
+ *   window        >= 0; 0: none
+ *   out           device bf16 rows like q, out_stride elements apart; must not
+ *                 overlap q
+ *   lse           device fp32 [num_tokens, num_q_heads], or NULL
+ *   workspace     device memory of at least fp4_kv_attention_workspace(...)
+ *                 bytes, 16-byte aligned.  It holds nothing between calls; two
+ *                 calls that may run at the same time need one each.
+ * Returns FP8Q_OK, FP8Q_EINVAL, FP8Q_ECUDA.
+ */
+FP8Q_API fp8q_status fp4_kv_attention(const void *q, int64_t q_stride, const void *k_pool,
+                                      const void *v_pool, int32_t block_size,
+                                      int64_t block_stride, int64_t num_blocks,
+                                      int32_t num_kv_heads, int32_t head_dim,
+                                      const int32_t *block_table, int64_t table_stride,
+                                      int64_t table_width, const int32_t *seq_lens,
+                                      const int32_t *q_start, int64_t batch, int64_t num_tokens,
+                                      int32_t num_q_heads, float softmax_scale, int64_t window,
+                                      float k_scale, float v_scale, const float *scale_dev,
+                                      void *out, int64_t out_stride, float *lse, void *workspace,
+                                      int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace fp4_kv_attention needs for these sizes; -1 for sizes it
+ * refuses. */
+FP8Q_API int64_t fp4_kv_attention_workspace(int64_t batch, int64_t num_tokens,
+                                            int32_t num_q_heads, int32_t num_kv_heads,
+                                            int32_t head_dim);
+
+/* ------------------------------------------------------------------------ */
+/* 5. Norms of queries and keys with the position rotation                  */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * qk_norm_rope -- for each token and head of q and k, in fp32:
+ *   y = x * (mean(x^2) + eps)^-1/2 * weight      without a weight y = x
+ *   (a, b) -> (a cos - b sin, b cos + a sin)     for rotary_dim / 2 pairs of y
+ * and one rounding to bf16.  Pair i is (y[i], y[i + rotary_dim / 2]), or
+ * (y[2i], y[2i + 1]) when interleaved; elements from rotary_dim on are passed
+ * through.  Its angle is positions[t] * inv_freq[i], reduced in fp64, and its
+ * cosine and sine are multiplied by rope_scale.
+ *
+ *   q, k          device bf16 [num_tokens, num_q_heads, head_dim] and
+ *                 [num_tokens, num_kv_heads, head_dim] rows, 16-byte aligned,
+ *                 q_stride and k_stride elements apart (multiples of 8)
+ *   q_out, k_out  like q and k, with strides of their own; an output may be
+ *                 its input (same address and stride) and must not overlap an
+ *                 input otherwise
+ *   positions     device int64 [num_tokens]
+ *   inv_freq      device fp64 [rotary_dim / 2] (may be NULL with rotary_dim 0)
+ *   q_weight,
+ *   k_weight      device bf16 [head_dim], 16-byte aligned, or NULL: no norm
+ *   num_tokens    0 .. 2^31 - 1; 0 is a no-op
+ *   num_q_heads,
+ *   num_kv_heads  >= 0, not both 0 and at most 65536 together; a tensor
+ *                 without heads may be NULL
+ *   head_dim      64, 128 or 256
+ *   rotary_dim    a multiple of 8 in [0, head_dim]
+ *   eps           finite, >= 0
+ *   rope_scale    finite
+ * Returns FP8Q_OK, FP8Q_EINVAL, FP8Q_ECUDA.
+ */
+FP8Q_API fp8q_status qk_norm_rope(const void *q, const void *k, int64_t q_stride,
+                                  int64_t k_stride, void *q_out, void *k_out,
+                                  int64_t q_out_stride, int64_t k_out_stride,
+                                  const int64_t *positions, const double *inv_freq,
+                                  const void *q_weight, const void *k_weight, int64_t num_tokens,
+                                  int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                  int32_t rotary_dim, int32_t interleaved, float eps,
+                                  float rope_scale, void *stream);
 
 /* ------------------------------------------------------------------------ */
 /* Diagnostics                                                              */

@@ -1,6 +1,7 @@
 """FP8 E4M3 quantization for B200: per-token 1x128-group activation
 quantization, the paged KV-cache quantize-and-scatter, and online calibration
-of the KV scales.
+of the KV scales; and a paged KV cache held in 4 bits: written, read back and
+attended to, with the norm and rotation of queries and keys before it.
 
 The compute is the CUDA library libfp8q.so (C ABI: include/fp8q.h).  This
 module only marshals torch tensors (device memory) and streams into those
@@ -14,8 +15,8 @@ import ctypes
 import torch
 
 from . import _abi
-from ._abi import (CALIB_STATE_BYTES, DEVERR_BAD_SCALE, DEVERR_SLOT_OUT_OF_RANGE,  # noqa: F401
-                   MAX_STAGED_TOKENS, PROVISIONAL_SCALE, STEP_FREEZE, STEP_FROZEN, STEP_STAGE,
+from ._abi import (CALIB_STATE_BYTES, DEVERR_BAD_SCALE, DEVERR_BAD_SEQUENCE,  # noqa: F401
+                   DEVERR_SLOT_OUT_OF_RANGE, DEVERR_WAIT, MAX_STAGED_TOKENS, PROVISIONAL_SCALE, STEP_FREEZE, STEP_FROZEN, STEP_STAGE,
                    STEP_STAGE_DECLINED, CalibStats, Fp8qError)
 
 lib = _abi.load()
@@ -386,6 +387,309 @@ def load_scales(path: str) -> list[tuple[float, float]]:
     with open(path) as fh:
         data = json.load(fh)["fp8_kv_scales"]
     return [(float.fromhex(d["k_scale"]), float.fromhex(d["v_scale"])) for d in data]
+
+
+# ---------------------------------------------------------------------------
+# the 4-bit paged KV cache
+
+
+def _rows3(t: torch.Tensor, name: str) -> int:
+    """Row stride in elements of a CUDA bf16 ``[T, heads, dim]`` tensor whose
+    rows are contiguous."""
+    if t.dtype != torch.bfloat16 or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA bfloat16 tensor")
+    n, heads, dim = t.shape
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and dim != 1) or (s1 != dim and heads != 1):
+        if t.numel():
+            raise ValueError(f"{name} rows must be contiguous")
+    return s0 if n > 1 else heads * dim
+
+
+def _same_device(device: int, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"{name} must be on the same CUDA device as the other tensors")
+
+
+def _call_on(device: int, stream, name: str, fn, *args) -> None:
+    """Call the library with ``device`` current; no stream given means the
+    current stream of that device."""
+    if stream is None:
+        raw = torch.cuda.current_stream(device).cuda_stream
+    else:
+        raw = stream if isinstance(stream, int) else stream.cuda_stream
+    if torch.cuda.current_device() == device:
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, raw)
+    if status != _abi.OK:
+        _check(name, status)
+
+
+def fp4_kv_pool_shape(num_blocks: int, block_size: int, num_kv_heads: int, head_dim: int):
+    """Shape of one 4-bit pool (uint8): a block holds ``block_size / 16`` tiles
+    of 16 tokens for each head, ``9 * head_dim`` bytes each (include/fp8q.h)."""
+    if block_size <= 0 or block_size % 16:
+        raise ValueError("block_size must be a positive multiple of 16")
+    if head_dim not in (64, 128, 256):
+        raise ValueError("head_dim must be 64, 128 or 256")
+    return num_blocks, num_kv_heads, block_size // 16, 9 * head_dim
+
+
+def fp4_kv_pools(num_blocks: int, block_size: int, num_kv_heads: int, head_dim: int, device="cuda"):
+    """A zeroed ``(k_pool, v_pool)`` pair of the 4-bit cache."""
+    shape = fp4_kv_pool_shape(num_blocks, block_size, num_kv_heads, head_dim)
+    return (torch.zeros(shape, dtype=torch.uint8, device=device),
+            torch.zeros(shape, dtype=torch.uint8, device=device))
+
+
+def _fp4_geometry(k_pool: torch.Tensor, v_pool: torch.Tensor):
+    """Pools ``[num_blocks, heads, block_size / 16, 9 * dim]`` (block stride may
+    be padded): (num_blocks, heads, block_size, dim, block stride in bytes)."""
+    if k_pool.dtype != torch.uint8 or v_pool.dtype != torch.uint8 or not k_pool.is_cuda \
+            or not v_pool.is_cuda:
+        raise TypeError("k_pool and v_pool must be CUDA uint8 tensors")
+    shape, stride = k_pool.shape, k_pool.stride()
+    if shape != v_pool.shape or stride != v_pool.stride():
+        raise ValueError("k_pool and v_pool must have the same shape and strides")
+    if len(shape) != 4 or shape[3] % 9:
+        raise ValueError("pools must be [num_blocks, num_kv_heads, block_size / 16, 9 * head_dim]")
+    num_blocks, heads, tiles, tile = shape
+    if num_blocks and (stride[3] != 1 or (tiles != 1 and stride[2] != tile)
+                       or (heads != 1 and stride[1] != tiles * tile)):
+        raise ValueError("each pool block must be contiguous")
+    return (num_blocks, heads, 16 * tiles, tile // 9,
+            stride[0] if num_blocks > 1 else heads * tiles * tile)
+
+
+def _fp4_rows(k: torch.Tensor, v: torch.Tensor, slot_mapping, k_pool, v_pool, scale_dev):
+    """Shared argument checks of fp4_kv_write and fp4_kv_read; their arguments
+    up to the scales."""
+    if k.dim() != 3 or k.shape != v.shape:
+        raise ValueError(f"k and v must both be [T, heads, dim] of one shape, got {tuple(k.shape)} "
+                         f"and {tuple(v.shape)}")
+    ks, vs = _rows3(k, "k"), _rows3(v, "v")
+    t, heads, dim = k.shape
+    _check_slots(slot_mapping, t)
+    _check_scale_pair(scale_dev, "scale_dev")
+    nb, pool_heads, bs, pool_dim, stride = _fp4_geometry(k_pool, v_pool)
+    if (heads, dim) != (pool_heads, pool_dim):
+        raise ValueError(f"pools hold {pool_heads} heads of {pool_dim}, k and v have {heads} of {dim}")
+    device = k.get_device()
+    _same_device(device, v=v, k_pool=k_pool, v_pool=v_pool, scale_dev=scale_dev,
+                 slot_mapping=slot_mapping if t else None)
+    return device, (k.data_ptr(), v.data_ptr(), ks, vs, slot_mapping.data_ptr(), t, heads, dim,
+                    k_pool.data_ptr(), v_pool.data_ptr(), bs, stride, nb)
+
+
+def fp4_kv_write(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
+                 k_pool: torch.Tensor, v_pool: torch.Tensor, k_scale: float = 1.0,
+                 v_scale: float = 1.0, scale_dev: torch.Tensor | None = None, stream=None) -> None:
+    """Quantise K, V ``[T, heads, dim]`` bf16 (rows may be strided) to 4 bits and
+    scatter them into the pools at ``slot_mapping`` (int64, negative skips)."""
+    device, args = _fp4_rows(k, v, slot_mapping, k_pool, v_pool, scale_dev)
+    _call_on(device, stream, "fp4_kv_write", lib.fp4_kv_write, *args, k_scale, v_scale,
+             _ptr(scale_dev))
+
+
+def fp4_kv_read(slot_mapping: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                k_scale: float = 1.0, v_scale: float = 1.0,
+                scale_dev: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+                v_out: torch.Tensor | None = None, stream=None):
+    """Gather the tokens at ``slot_mapping`` back as bf16 ``[T, heads, dim]``.
+    Rows of negative slots keep what ``k_out`` and ``v_out`` held (zeros when
+    they are allocated here)."""
+    if k_out is None or v_out is None:
+        _, heads, _, dim, _ = _fp4_geometry(k_pool, v_pool)
+        shape = (slot_mapping.numel(), heads, dim)
+        with _allocating_for(stream, k_pool.device):
+            if k_out is None:
+                k_out = torch.zeros(shape, dtype=torch.bfloat16, device=k_pool.device)
+            if v_out is None:
+                v_out = torch.zeros(shape, dtype=torch.bfloat16, device=k_pool.device)
+    device, args = _fp4_rows(k_out, v_out, slot_mapping, k_pool, v_pool, scale_dev)
+    _call_on(device, stream, "fp4_kv_read", lib.fp4_kv_read, *args, k_scale, v_scale,
+             _ptr(scale_dev))
+    return k_out, v_out
+
+
+def _allocating_for(stream, device: torch.device):
+    """Context in which tensors belong to ``stream``, so that their memory is
+    not handed out again before the stream's work on them is done."""
+    if stream is None:
+        return torch.cuda.device(device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    return torch.cuda.stream(stream)
+
+
+def _check_index(t: torch.Tensor, name: str, *shape) -> None:
+    if t.dtype != torch.int32 or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be int32 {list(shape)}")
+
+
+def fp4_kv_attention_workspace(batch: int, num_tokens: int, num_q_heads: int, num_kv_heads: int,
+                               head_dim: int) -> int:
+    """Bytes of workspace fp4_kv_attention needs for these sizes."""
+    n = lib.fp4_kv_attention_workspace(batch, num_tokens, num_q_heads, num_kv_heads, head_dim)
+    if n < 0:
+        raise ValueError("sizes fp4_kv_attention does not take")
+    return n
+
+
+def fp4_kv_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                     block_table: torch.Tensor, seq_lens: torch.Tensor,
+                     softmax_scale: float | None = None, q_start: torch.Tensor | None = None,
+                     window: int = 0, k_scale: float = 1.0, v_scale: float = 1.0,
+                     scale_dev: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                     lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                     stream=None):
+    """Causal attention of the new tokens ``q [T, q_heads, dim]`` (bf16, rows may
+    be strided) over the 4-bit cache.
+
+    ``seq_lens`` int32 ``[batch]`` counts each sequence's cached tokens, the new
+    ones included; ``block_table`` int32 ``[batch, width]`` lists its blocks;
+    ``q_start`` int32 ``[batch + 1]`` says where its rows of q begin (None: one
+    new token each).  A new token sees the cached tokens up to itself, of them
+    only the last ``window`` when that is positive.  ``softmax_scale`` defaults
+    to dim ** -0.5.  Returns ``out``, or ``(out, lse)`` when an fp32 ``lse
+    [T, q_heads]`` is given to be filled.  ``workspace`` (uint8, at least
+    fp4_kv_attention_workspace() bytes) is allocated for the call when not
+    given; calls that may overlap need one each."""
+    if q.dim() != 3:
+        raise ValueError("q must be [T, heads, dim]")
+    q_stride = _rows3(q, "q")
+    t, q_heads, dim = q.shape
+    nb, heads, bs, pool_dim, stride = _fp4_geometry(k_pool, v_pool)
+    if dim != pool_dim or heads == 0 or q_heads % heads:
+        raise ValueError(f"pools hold {heads} heads of {pool_dim}, q has {q_heads} of {dim}")
+    batch = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
+    _check_index(seq_lens, "seq_lens", batch)
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != batch:
+        raise ValueError("block_table must be int32 [batch, width]")
+    width = block_table.shape[1]
+    if block_table.stride(1) != 1 and width > 1:
+        raise ValueError("block_table rows must be contiguous")
+    table_stride = block_table.stride(0) if batch > 1 else width
+    if batch > 1 and seq_lens.stride(0) != 1:
+        raise ValueError("seq_lens must be contiguous")
+    if q_start is not None:
+        _check_index(q_start, "q_start", batch + 1)
+        if batch and q_start.stride(0) != 1:
+            raise ValueError("q_start must be contiguous")
+    elif t != batch:
+        raise ValueError("without q_start, q must have one row for each sequence")
+    _check_scale_pair(scale_dev, "scale_dev")
+    device = q.get_device()
+    if out is None or workspace is None:
+        with _allocating_for(stream, q.device):
+            if out is None:
+                out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+            if workspace is None:
+                workspace = torch.empty(fp4_kv_attention_workspace(batch, t, q_heads, heads, dim),
+                                        dtype=torch.uint8, device=q.device)
+    if out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    out_stride = _rows3(out, "out")
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (t, q_heads)
+                            or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 tensor [T, q_heads]")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _same_device(device, k_pool=k_pool, v_pool=v_pool, block_table=block_table, seq_lens=seq_lens,
+                 q_start=q_start, scale_dev=scale_dev, out=out, lse=lse, workspace=workspace)
+    _call_on(device, stream, "fp4_kv_attention", lib.fp4_kv_attention,
+             q.data_ptr(), q_stride, k_pool.data_ptr(), v_pool.data_ptr(), bs, stride, nb, heads,
+             dim, block_table.data_ptr(), table_stride, width, seq_lens.data_ptr(), _ptr(q_start),
+             batch, t, q_heads, dim ** -0.5 if softmax_scale is None else softmax_scale, window,
+             k_scale, v_scale, _ptr(scale_dev), out.data_ptr(), out_stride, _ptr(lse),
+             workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return out if lse is None else (out, lse)
+
+
+# ---------------------------------------------------------------------------
+# norms of queries and keys with the position rotation
+
+
+def rope_inv_freq(rotary_dim: int, base: float = 10000.0, stretch: float = 1.0,
+                  trained_length: int | None = None, fast: float = 32.0, slow: float = 1.0,
+                  device="cuda") -> torch.Tensor:
+    """Rotation frequencies ``base ** (-2i / rotary_dim)``, fp64
+    ``[rotary_dim / 2]``, for contexts ``stretch`` times as long as the trained
+    ones.  Without ``trained_length`` every frequency is divided by ``stretch``
+    (positions interpolated).  With it, frequencies that turn at least ``fast``
+    times over the trained length stay, those that turn at most ``slow`` times
+    are divided, and the ones between are blended linearly in their index
+    (interpolation by parts, as YaRN does)."""
+    if rotary_dim < 0 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even")
+    if not (base > 1 and stretch >= 1):
+        raise ValueError("base must be > 1 and stretch >= 1")
+    import math
+    freq = [base ** (-2.0 * i / rotary_dim) for i in range(rotary_dim // 2)]
+    if trained_length is None:
+        keep = [0.0] * len(freq)
+    else:
+        if not (trained_length > 0 and fast > slow > 0):
+            raise ValueError("trained_length must be > 0 and fast > slow > 0")
+
+        def index(turns):      # where a frequency turns that often over trained_length
+            return rotary_dim * math.log(trained_length / (turns * 2 * math.pi)) / (2 * math.log(base))
+
+        lo = max(math.floor(index(fast)), 0)
+        hi = max(min(math.ceil(index(slow)), rotary_dim - 1), lo + 0.001)
+        keep = [1.0 - min(max((i - lo) / (hi - lo), 0.0), 1.0) for i in range(len(freq))]
+    return torch.tensor([f * (w + (1.0 - w) / stretch) for f, w in zip(freq, keep)],
+                        dtype=torch.float64, device=device)
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor,
+                 inv_freq: torch.Tensor, q_weight: torch.Tensor | None = None,
+                 k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                 interleaved: bool = False, rope_scale: float = 1.0,
+                 q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+                 stream=None):
+    """Root-mean-square norm of each head of ``q [T, q_heads, dim]`` and ``k
+    [T, kv_heads, dim]`` (bf16, rows may be strided; no norm without a weight),
+    then the rotation of its first ``2 * len(inv_freq)`` elements by
+    ``positions[t] * inv_freq`` (fp64): halves paired, or neighbours when
+    ``interleaved``.  ``rope_scale`` multiplies cosine and sine.  ``q_out`` and
+    ``k_out`` may be ``q`` and ``k``."""
+    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+        raise ValueError(f"q and k must be [T, heads, dim] with the same T and dim, got "
+                         f"{tuple(q.shape)} and {tuple(k.shape)}")
+    q_stride, k_stride = _rows3(q, "q"), _rows3(k, "k")
+    t, q_heads, dim = q.shape
+    k_heads = k.shape[1]
+    if positions.dtype != torch.int64 or tuple(positions.shape) != (t,) or \
+            (t > 1 and positions.stride(0) != 1):
+        raise ValueError("positions must be a contiguous int64 tensor [T]")
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous float64 tensor [rotary_dim / 2]")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None and (w.dtype != torch.bfloat16 or tuple(w.shape) != (dim,)
+                              or not w.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous bfloat16 tensor [dim]")
+    device = q.get_device()
+    if q_out is None or k_out is None:
+        with _allocating_for(stream, q.device):
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+            if k_out is None:
+                k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
+    if q_out.shape != q.shape or k_out.shape != k.shape:
+        raise ValueError("q_out and k_out must have the shapes of q and k")
+    qo_stride, ko_stride = _rows3(q_out, "q_out"), _rows3(k_out, "k_out")
+    _same_device(device, k=k, positions=positions, inv_freq=inv_freq, q_weight=q_weight,
+                 k_weight=k_weight, q_out=q_out, k_out=k_out)
+    _call_on(device, stream, "qk_norm_rope", lib.qk_norm_rope,
+             q.data_ptr(), k.data_ptr(), q_stride, k_stride, q_out.data_ptr(), k_out.data_ptr(),
+             qo_stride, ko_stride, positions.data_ptr(), inv_freq.data_ptr(), _ptr(q_weight),
+             _ptr(k_weight), t, q_heads, k_heads, dim, 2 * inv_freq.shape[0], int(interleaved),
+             eps, rope_scale)
+    return q_out, k_out
 
 
 def fp8q_device_error(clear: bool = True) -> int:

@@ -73,6 +73,16 @@ SIGNATURES = {
     "fp8_kv_graphs_ready": (_I32, [_P, _I64]),
     "fp8_kv_calib_window_noalloc": (STATUS, [_P, _P, _I64, _I64, _P, _P, _I32, _I32, _I32, _I64,
                                              _F, _P, _P, _I32, _I64, _I64, _P, _P]),
+    "fp4_kv_write": (STATUS, [_P, _P, _I64, _I64, _P, _I64, _I32, _I32, _P, _P, _I32, _I64, _I64,
+                              _F, _F, _P, _P]),
+    "fp4_kv_read": (STATUS, [_P, _P, _I64, _I64, _P, _I64, _I32, _I32, _P, _P, _I32, _I64, _I64,
+                             _F, _F, _P, _P]),
+    "fp4_kv_attention": (STATUS, [_P, _I64, _P, _P, _I32, _I64, _I64, _I32, _I32, _P, _I64, _I64,
+                                  _P, _P, _I64, _I64, _I32, _F, _I64, _F, _F, _P, _P, _I64, _P,
+                                  _P, _I64, _P]),
+    "fp4_kv_attention_workspace": (_I64, [_I64, _I64, _I32, _I32, _I32]),
+    "qk_norm_rope": (STATUS, [_P, _P, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _P, _P, _I64, _I32,
+                              _I32, _I32, _I32, _I32, _F, _F, _P]),
     "fp8q_device_error": (STATUS, [c.POINTER(c.c_uint32), _I32]),
     "fp8q_status_string": (c.c_char_p, [STATUS]),
     "fp8q_version": (_I32, []),
@@ -82,6 +92,7 @@ SIGNATURES = {
 OK, EINVAL, ECUDA, ESTATE, ENOMEM, ETOOBIG = 0, -1, -2, -3, -4, -5
 STEP_STAGE, STEP_STAGE_DECLINED, STEP_FREEZE, STEP_FROZEN = 1, 2, 3, 4
 DEVERR_SLOT_OUT_OF_RANGE, DEVERR_BAD_SCALE = 0x1, 0x2
+DEVERR_BAD_SEQUENCE, DEVERR_WAIT = 0x4, 0x8
 MAX_STAGED_TOKENS = 4096
 PROVISIONAL_SCALE = 2.0
 CALIB_STATE_BYTES = 16

@@ -1,0 +1,242 @@
+// fp4_kv.cu -- K and V quantised to 4 bits as they are scattered into a paged
+// cache, and gathered back as bf16 (sm_100a).
+//
+// A block of 16 neighbouring dimensions of one token's head shares an E4M3
+// scale b under the tensor's fp32 scale s; with amax the block's largest |x|:
+//     b = E4M3(RN(RN(amax / 6) / s)),  d = RN(b * s),  r = RN(1 / d)  (0 if d = 0)
+//     code = E2M1(RN(x * r));          value = RN(code * b * s) -> bf16
+// code * b has at most six significant bits and lies in [2^-10, 2688], so it
+// is exact in fp16; only the product with s and the bf16 result round.
+//
+// Both kernels are bound by memory traffic: 2 bytes of bf16 on one side and
+// 9/16 byte of cache on the other, with about two instructions an element.
+// One thread owns one 16-element block of K and the same block of V: four
+// 16-byte accesses in flight on the bf16 side, an 8-byte code word and a
+// scale byte on the cache side, and no exchange between threads.
+#include <cuda_runtime.h>
+
+#include "fp4_device.cuh"
+
+namespace fp8q {
+
+namespace {
+
+__device__ uint32_t g_fp4_kv_error;
+
+constexpr int kThreads = 256;
+
+// Where a block's code word and scale byte lie in a pool's tile of 16 tokens:
+// K token-major, V block-major (the layouts attention reads fragments from).
+struct BlockPlace {
+    int64_t tile;        // byte offset of the tile in the pool
+    uint32_t k_code, k_scale, v_code, v_scale;
+};
+
+template <int D>
+__device__ __forceinline__ BlockPlace block_place(const Fp4Pools &p, int64_t slot, int32_t head,
+                                                  int32_t block) {
+    const int32_t block_size = p.tiles * 16;
+    const int64_t page = slot / block_size;
+    const int32_t off = static_cast<int32_t>(slot - page * block_size);
+    const uint32_t tok = off & 15;
+    BlockPlace b;
+    b.tile = page * p.block_stride + (static_cast<int64_t>(head) * p.tiles + (off >> 4)) * (9 * D);
+    b.k_code = tok * (D / 2) + block * 8;
+    b.k_scale = 8 * D + tok * (D / 16) + block;
+    b.v_code = block * 128 + tok * 8;
+    b.v_scale = 8 * D + block * 16 + tok;
+    return b;
+}
+
+// Block index -> (token, head, block of the head).
+template <int D>
+__device__ __forceinline__ void split_index(uint32_t i, int32_t heads, uint32_t *token,
+                                            int32_t *head, int32_t *block) {
+    const uint32_t row = i / (D / 16);
+    *block = static_cast<int32_t>(i % (D / 16));
+    *token = row / static_cast<uint32_t>(heads);
+    *head = static_cast<int32_t>(row - *token * static_cast<uint32_t>(heads));
+}
+
+__device__ __forceinline__ void load_scales(const Fp4Pools &p, float *ks, float *vs) {
+    *ks = p.scale_dev ? p.scale_dev[0] : p.k_scale;
+    *vs = p.scale_dev ? p.scale_dev[1] : p.v_scale;
+}
+
+// 16 bf16 values (two 16-byte words) to a code word and a scale byte.
+__device__ __forceinline__ uint2 quantise16(const uint4 &a, const uint4 &b, float scale,
+                                            uint32_t *scale_code) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    float x[16];
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        x[2 * i] = bf16_low(w[i]);
+        x[2 * i + 1] = bf16_high(w[i]);
+        amax = fmaxf(amax, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
+    }
+    const float t = __fdiv_rn(__fdiv_rn(amax, 6.0f), scale);
+    unsigned short code;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(code) : "f"(0.0f), "f"(t));
+    *scale_code = code & 0xFFu;
+    float block_scale;
+    {
+        const uint32_t h = f16x2_of_e4m3x2(code) & 0xFFFFu;
+        asm("cvt.f32.f16 %0, %1;" : "=f"(block_scale) : "h"(static_cast<unsigned short>(h)));
+    }
+    const float d = __fmul_rn(block_scale, scale);
+    const float r = d > 0.0f ? __frcp_rn(d) : 0.0f;
+    float lo[8], hi[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        lo[i] = __fmul_rn(x[i], r);
+        hi[i] = __fmul_rn(x[8 + i], r);
+    }
+    return make_uint2(e2m1x8_of(lo), e2m1x8_of(hi));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) fp4_write_kernel(const Fp4Rows r, const Fp4Pools p,
+                                                             uint32_t blocks) {
+    pdl_wait();
+    pdl_allow_next();
+    const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
+    if (i >= blocks) return;
+    uint32_t token;
+    int32_t head, block;
+    split_index<D>(i, p.heads, &token, &head, &block);
+    const int64_t slot = r.slots[token];
+    if (slot < 0) return;
+    if (slot >= p.num_blocks * (p.tiles * 16)) {
+        atomicOr(&g_fp4_kv_error, kFp4ErrSlot);
+        return;
+    }
+    const int32_t e = head * D + block * 16;
+    const uint4 *k = reinterpret_cast<const uint4 *>(r.k + token * r.key_stride + e);
+    const uint4 *v = reinterpret_cast<const uint4 *>(r.v + token * r.value_stride + e);
+    const uint4 k0 = __ldcs(k), k1 = __ldcs(k + 1), v0 = __ldcs(v), v1 = __ldcs(v + 1);
+    float ks, vs;
+    load_scales(p, &ks, &vs);
+    const BlockPlace at = block_place<D>(p, slot, head, block);
+    const bool k_ok = fp4_scale_ok(ks), v_ok = fp4_scale_ok(vs);
+    if (!k_ok || !v_ok) atomicOr(&g_fp4_kv_error, kFp4ErrScale);
+    uint32_t sc;
+    if (k_ok) {
+        const uint2 c = quantise16(k0, k1, ks, &sc);
+        *reinterpret_cast<uint2 *>(p.k + at.tile + at.k_code) = c;
+        p.k[at.tile + at.k_scale] = static_cast<uint8_t>(sc);
+    }
+    if (v_ok) {
+        const uint2 c = quantise16(v0, v1, vs, &sc);
+        *reinterpret_cast<uint2 *>(p.v + at.tile + at.v_code) = c;
+        p.v[at.tile + at.v_scale] = static_cast<uint8_t>(sc);
+    }
+}
+
+__device__ __forceinline__ void dequantise16(uint2 codes, uint32_t scale_code, float scale,
+                                             uint4 *a, uint4 *b) {
+    const uint32_t s2 = f16x2_of_e4m3x2(scale_code | scale_code << 8);
+    uint32_t w[8];
+    uint32_t h[4];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        f16x2_of_e2m1x8(half ? codes.y : codes.x, h);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t m = mul_f16x2(h[i], s2);
+            float lo, hi;
+            asm("{\n\t.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+                "cvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}" : "=f"(lo), "=f"(hi) : "r"(m));
+            w[4 * half + i] = bf16x2_of(__fmul_rn(lo, scale), __fmul_rn(hi, scale));
+        }
+    }
+    *a = make_uint4(w[0], w[1], w[2], w[3]);
+    *b = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) fp4_read_kernel(const Fp4Rows r, const Fp4Pools p,
+                                                            uint32_t blocks) {
+    pdl_wait();
+    pdl_allow_next();
+    const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
+    if (i >= blocks) return;
+    uint32_t token;
+    int32_t head, block;
+    split_index<D>(i, p.heads, &token, &head, &block);
+    const int64_t slot = r.slots[token];
+    if (slot < 0) return;
+    if (slot >= p.num_blocks * (p.tiles * 16)) {
+        atomicOr(&g_fp4_kv_error, kFp4ErrSlot);
+        return;
+    }
+    const BlockPlace at = block_place<D>(p, slot, head, block);
+    const uint2 kc = *reinterpret_cast<const uint2 *>(p.k + at.tile + at.k_code);
+    const uint2 vc = *reinterpret_cast<const uint2 *>(p.v + at.tile + at.v_code);
+    const uint32_t kb = p.k[at.tile + at.k_scale], vb = p.v[at.tile + at.v_scale];
+    float ks, vs;
+    load_scales(p, &ks, &vs);
+    const bool k_ok = fp4_scale_ok(ks), v_ok = fp4_scale_ok(vs);
+    if (!k_ok || !v_ok) atomicOr(&g_fp4_kv_error, kFp4ErrScale);
+    const int32_t e = head * D + block * 16;
+    uint4 a, b;
+    if (k_ok) {
+        dequantise16(kc, kb, ks, &a, &b);
+        uint4 *k = reinterpret_cast<uint4 *>(r.k + token * r.key_stride + e);
+        k[0] = a;
+        k[1] = b;
+    }
+    if (v_ok) {
+        dequantise16(vc, vb, vs, &a, &b);
+        uint4 *v = reinterpret_cast<uint4 *>(r.v + token * r.value_stride + e);
+        v[0] = a;
+        v[1] = b;
+    }
+}
+
+// Block indexes are 32 bits inside a launch; more tokens than that take
+// several launches.
+template <typename Kernel>
+cudaError_t launch_rows(Kernel kernel, Fp4Rows r, const Fp4Pools &p, cudaStream_t stream) {
+    const int64_t per_token = static_cast<int64_t>(p.heads) * (p.dim / 16);
+    const int64_t most = (int64_t{1} << 30) / per_token;
+    while (r.num_tokens > 0) {
+        const int64_t n = r.num_tokens < most ? r.num_tokens : most;
+        const uint32_t blocks = static_cast<uint32_t>(n * per_token);
+        const cudaError_t e = launch_pdl(kernel, dim3((blocks + kThreads - 1) / kThreads), kThreads,
+                                         0, stream, r, p, blocks);
+        if (e != cudaSuccess) return e;
+        r.num_tokens -= n;
+        r.k += n * r.key_stride;
+        r.v += n * r.value_stride;
+        r.slots += n;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_fp4_write(const Fp4Rows &r, const Fp4Pools &p, cudaStream_t stream) {
+    return launch_rows(p.dim == 64    ? fp4_write_kernel<64>
+                       : p.dim == 128 ? fp4_write_kernel<128>
+                                      : fp4_write_kernel<256>,
+                       r, p, stream);
+}
+
+cudaError_t launch_fp4_read(const Fp4Rows &r, const Fp4Pools &p, cudaStream_t stream) {
+    return launch_rows(p.dim == 64    ? fp4_read_kernel<64>
+                       : p.dim == 128 ? fp4_read_kernel<128>
+                                      : fp4_read_kernel<256>,
+                       r, p, stream);
+}
+
+cudaError_t read_fp4_kv_error(uint32_t *bits, bool clear) {
+    cudaError_t e = cudaMemcpyFromSymbol(bits, g_fp4_kv_error, sizeof(uint32_t));
+    if (e == cudaSuccess && clear) {
+        const uint32_t zero = 0;
+        e = cudaMemcpyToSymbol(g_fp4_kv_error, &zero, sizeof(uint32_t));
+    }
+    return e;
+}
+
+}  // namespace fp8q
