@@ -1,0 +1,263 @@
+// How attention over the 4-bit cache is divided among the blocks of a launch.
+//
+// An item is one (sequence, KV head, tile of query rows).  It is made of units
+// of kUnit cached tokens, counted from the first token its own rows see, and
+// costs its units plus kItemCost: loading the rows and finishing the sums take
+// about as long as a unit.  Items are laid side by side on one axis, every
+// block takes an equal run of it, and unit j of an item lies at the point
+// item start + kItemCost + j.  A block finds its run from the lengths on the
+// device, so a launch depends on sizes alone and may be captured.
+//
+// An item whose units lie in several blocks leaves one part in each: blocks
+// behind the first leave part 0, the first one part 1 and a record of the item,
+// from which the join merges the parts in a fixed order.
+#pragma once
+
+#include "fp4_device.cuh"
+
+namespace fp8q {
+namespace fp4_plan {
+
+constexpr int kUnit = 128;             // cached tokens of a unit
+constexpr int kItemCost = 1;           // units an item costs beside its own
+constexpr int kMaxBlocks = 592;        // blocks a workspace has room for
+
+// One sequence as the kernels see it: bad lengths and ranges are cut to what
+// the buffers hold and reported.
+struct Sequence {
+    int32_t token0;     // first new token
+    int32_t news;       // new tokens
+    int32_t length;     // cached tokens, the new ones included
+    int32_t row_tiles;
+};
+
+__device__ __forceinline__ Sequence sequence(const Fp4Attention &a, int32_t b, int32_t group,
+                                             int32_t tile_rows, bool *bad) {
+    Sequence s;
+    int64_t t0 = b, t1 = b + 1;
+    if (a.q_start != nullptr) {
+        t0 = a.q_start[b];
+        t1 = a.q_start[b + 1];
+    }
+    int64_t length = a.seq_lens[b];
+    if (t0 < 0 || t1 < t0 || t1 > a.num_tokens) {
+        *bad = true;
+        t0 = t0 < 0 ? 0 : t0;
+        t1 = t1 > a.num_tokens ? a.num_tokens : t1;
+        if (t1 < t0) t0 = t1 = 0;
+    }
+    const int64_t room = a.pools.num_blocks > 0 ? a.table_width * (a.pools.tiles * 16) : 0;
+    if (length < 0 || length > room) {
+        *bad = true;
+        length = length < 0 ? 0 : room;
+    }
+    s.token0 = static_cast<int32_t>(t0);
+    s.news = static_cast<int32_t>(t1 - t0);
+    s.length = static_cast<int32_t>(length);
+    // rows of a call stay within 2^30
+    s.row_tiles = (s.news * group + tile_rows - 1) / tile_rows;
+    return s;
+}
+
+// The rows of one tile of a sequence and the cached tokens they see.
+struct Tile {
+    int32_t row0, rows;
+    int32_t first;      // the first token any row sees
+    int32_t begin;      // ... rounded down to 16 slots: where units count from
+    int32_t end;        // behind the last token any row sees; >= begin
+    int32_t units;      // at least one
+};
+
+__device__ __forceinline__ Tile tile_of(const Sequence &s, int32_t rt, int32_t group,
+                                        int32_t tile_rows, int32_t window) {
+    Tile x;
+    x.row0 = rt * tile_rows;
+    x.rows = min(tile_rows, s.news * group - x.row0);
+    const int32_t ahead = s.length - s.news;   // query i sees tokens up to ahead + i
+    const int32_t q_lo = x.row0 / group, q_hi = (x.row0 + x.rows - 1) / group;
+    x.first = window > 0 ? max(0, ahead + q_lo + 1 - window) : 0;
+    x.begin = x.first & ~15;
+    x.end = max(x.begin, min(s.length, ahead + q_hi + 1));
+    x.units = max(1, (x.end - x.begin + kUnit - 1) / kUnit);
+    return x;
+}
+
+// Cost of all row tiles of one head, of a whole warp's sequences at once: few
+// tiles are summed by the lane that has the sequence, many by all lanes.
+__device__ __forceinline__ int64_t head_cost(const Sequence &mine, int32_t group, int32_t tile_rows,
+                                             int32_t window) {
+    constexpr int32_t kFew = 4;
+    const int32_t lane = threadIdx.x % 32;
+    int64_t cost = 0;
+    if (mine.row_tiles <= kFew)
+        for (int32_t rt = 0; rt < mine.row_tiles; ++rt)
+            cost += tile_of(mine, rt, group, tile_rows, window).units + kItemCost;
+    for (uint32_t many = __ballot_sync(0xFFFFFFFFu, mine.row_tiles > kFew); many; many &= many - 1) {
+        const int32_t from = __ffs(many) - 1;
+        Sequence s;
+        s.token0 = 0;
+        s.news = __shfl_sync(0xFFFFFFFFu, mine.news, from);
+        s.length = __shfl_sync(0xFFFFFFFFu, mine.length, from);
+        s.row_tiles = __shfl_sync(0xFFFFFFFFu, mine.row_tiles, from);
+        int64_t sum = 0;
+        for (int32_t rt = lane; rt < s.row_tiles; rt += 32)
+            sum += tile_of(s, rt, group, tile_rows, window).units + kItemCost;
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (lane == from) cost = sum;
+    }
+    return cost;
+}
+
+template <int kWarps>
+struct PlanShared {
+    int64_t scan[kWarps];
+    int64_t base;
+    int32_t seq;
+};
+
+// A block's run of the axis and where it starts.
+struct Run {
+    int64_t at, end;     // [at, end); empty: no work
+    int64_t per_block;
+    int64_t base;        // start of sequence `seq` on the axis
+    int32_t seq;
+};
+
+// Called by all kWarps warps of the block; holds two block barriers (one when
+// the run is empty).
+template <int kWarps>
+__device__ __forceinline__ Run block_run(const Fp4Attention &a, int32_t group, int32_t tile_rows,
+                                         uint32_t *error, PlanShared<kWarps> &sm) {
+    constexpr int32_t kThreads = 32 * kWarps;
+    const int32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int32_t per_thread = (a.batch + kThreads - 1) / kThreads;
+    const int64_t b0 = static_cast<int64_t>(threadIdx.x) * per_thread;
+    Sequence none;
+    none.token0 = none.news = none.length = none.row_tiles = 0;
+    bool bad = false;
+    int64_t mine = 0;
+    for (int32_t i = 0; i < per_thread; ++i) {
+        const Sequence s = b0 + i < a.batch
+            ? sequence(a, static_cast<int32_t>(b0 + i), group, tile_rows, &bad) : none;
+        mine += head_cost(s, group, tile_rows, a.window) * a.pools.heads;
+    }
+    if (bad) atomicOr(error, kFp4ErrSequence);
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int64_t up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += up;
+    }
+    if (lane == 31) sm.scan[warp] = incl;
+    __syncthreads();
+    int64_t before = incl - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += sm.scan[w];
+        total += sm.scan[w];
+    }
+    Run r;
+    r.per_block = (total + gridDim.x - 1) / gridDim.x;
+    r.at = r.per_block * blockIdx.x;
+    r.end = min(total, r.at + r.per_block);
+    r.seq = 0;
+    r.base = 0;
+    if (r.at >= r.end) return r;
+    const bool here = mine > 0 && before <= r.at && r.at < before + mine;
+    if (__any_sync(0xFFFFFFFFu, here)) {
+        for (int32_t i = 0; i < per_thread; ++i) {
+            const Sequence s = b0 + i < a.batch
+                ? sequence(a, static_cast<int32_t>(b0 + i), group, tile_rows, &bad) : none;
+            const int64_t n = head_cost(s, group, tile_rows, a.window) * a.pools.heads;
+            if (here && before <= r.at && r.at < before + n) {
+                sm.seq = static_cast<int32_t>(b0 + i);
+                sm.base = before;
+            }
+            before += n;
+        }
+    }
+    __syncthreads();
+    r.seq = sm.seq;
+    r.base = sm.base;
+    return r;
+}
+
+// Walks the items of a run, one warp; every lane holds the same state.
+struct Walk {
+    Sequence s;
+    int32_t seq, head, rt;
+    int64_t start;      // of the item on the axis
+
+    __device__ __forceinline__ void begin(const Fp4Attention &a, const Run &r, int32_t group,
+                                          int32_t tile_rows) {
+        const int32_t lane = threadIdx.x % 32;
+        bool bad = false;
+        seq = r.seq;
+        s = sequence(a, seq, group, tile_rows, &bad);
+        Sequence own = s;
+        if (lane != 0) own.row_tiles = 0;
+        const int64_t cost = __shfl_sync(0xFFFFFFFFu, head_cost(own, group, tile_rows, a.window), 0);
+        head = static_cast<int32_t>((r.at - r.base) / cost);
+        start = r.base + head * cost;
+        rt = 0;
+        for (int32_t first = 0;; first += 32) {   // the tile that holds r.at
+            int32_t n = 0;
+            if (first + lane < s.row_tiles)
+                n = tile_of(s, first + lane, group, tile_rows, a.window).units + kItemCost;
+            int64_t incl = n;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const int64_t up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+                if (lane >= o) incl += up;
+            }
+            const uint32_t beyond = __ballot_sync(0xFFFFFFFFu, n > 0 && start + incl > r.at);
+            if (beyond) {
+                const int32_t at = __ffs(beyond) - 1;
+                rt = first + at;
+                start += __shfl_sync(0xFFFFFFFFu, incl - n, at);
+                return;
+            }
+            start += __shfl_sync(0xFFFFFFFFu, incl, 31);
+            if (first + 32 >= s.row_tiles) return;    // not reached: the run starts in this head
+        }
+    }
+
+    // To the next item; `cost` is the present one's.  False behind the last.
+    __device__ __forceinline__ bool next(const Fp4Attention &a, int64_t cost, int32_t group,
+                                         int32_t tile_rows) {
+        start += cost;
+        if (++rt < s.row_tiles) return true;
+        rt = 0;
+        if (++head < a.pools.heads) return true;
+        head = 0;
+        bool bad = false;
+        do {
+            if (++seq >= a.batch) return false;
+            s = sequence(a, seq, group, tile_rows, &bad);
+        } while (s.row_tiles == 0);
+        return true;
+    }
+};
+
+// A block's record of the item that begins in it and goes on in the blocks
+// behind it.
+struct Split {
+    int32_t blocks;     // blocks that hold a part of the item; 0: no such item
+    int32_t token0, row0, rows, head;
+};
+
+// Workspace: Split [kMaxBlocks], then two parts for each block: rows x dim
+// sums, rows maxima and rows sums of weights.
+__host__ __device__ constexpr int64_t part_floats(int rows, int dim) {
+    return static_cast<int64_t>(rows) * (dim + 2);
+}
+constexpr int64_t kRecordBytes = (kMaxBlocks * sizeof(Split) + 15) / 16 * 16;
+
+__device__ __forceinline__ float *part_at(void *workspace, int64_t index, int rows, int dim) {
+    return reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kRecordBytes) +
+           index * part_floats(rows, dim);
+}
+
+}  // namespace fp4_plan
+}  // namespace fp8q
