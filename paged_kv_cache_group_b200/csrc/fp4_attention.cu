@@ -32,8 +32,14 @@
 // product for each pair of codes; the rest is kept off the four warps that do
 // it.  A fifth warp looks up pages and copies tiles ahead of them, across the
 // items of the block too, so that the next sequence's tokens are under way
-// while this one's sums are finished.  The running maximum is joined over
-// lanes only when some lane sees a larger score.
+// while this one's sums are finished.  It is the copies that have to be few:
+// of 1152 bytes each (16 tokens of one head of 128) the copying warps kept
+// 4.1 TB/s whether or not anything was computed.  So a block takes four, two or one
+// heads at once, whatever divides their number, with one, two or four of its
+// warps on each: the heads of a page lie side by side, and one copy takes all
+// of them when a page is 16 tokens, or 32 tokens of one when it is longer.
+// The running maximum is joined over lanes only when some lane sees a larger
+// score.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -87,6 +93,14 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+                 "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     uint32_t d;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -104,7 +118,6 @@ using namespace fp4_plan;
 constexpr int kWarps = 4;              // warps that compute
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kStep = 32;              // cached tokens of a warp's step
-static_assert(kStep * kWarps == kUnit, "a unit is one step of every warp");
 
 __device__ __forceinline__ void barrier_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
@@ -144,31 +157,40 @@ __device__ __forceinline__ uint32_t high_twice(uint32_t w) {
 
 // What the copying warp tells the others about an item.
 struct Item {
-    int32_t steps;              // 32-token steps of this block's part; -1: no more items
+    int32_t rounds;             // steps of every warp in this block's part; -1: no more items
     int32_t begin, end, first;  // its cached tokens, and the first one any row sees
     int32_t ahead;              // query i sees tokens up to ahead + i
-    int32_t token0, row0, rows, head;
+    int32_t token0, row0, rows;
+    int32_t set;                // its heads: kHeads * set and on
     int32_t part;               // -1: the whole item, else which of the block's parts
 };
 
-template <int D, int NT>
+// T warps share a head and take steps in turn; a block has 4 / T heads.
+template <int D, int NT, int T>
 struct Shape {
     static constexpr int kRows = 8 * NT;
+    static constexpr int kHeads = kWarps / T;
     static constexpr int kTile = 9 * D;                  // bytes of 16 tokens of a head
     static constexpr int kMTiles = D / 16;               // of O^T
+    static constexpr int kOwn = kMTiles / T;             // ... that each warp finishes
+    static constexpr int kUnit = kStep * T;              // cached tokens of a round
     static constexpr int kBlocks = NT * D <= 128 ? 3 : 2;   // an SM holds: by registers
-    static constexpr int kStages = D == 64 ? 5 : D == 128 ? 3 : 2;
+    static constexpr int kStages = D == 64 ? 5 : D == 256 ? 2 : NT == 1 ? 3 : 4;
     static constexpr int kQPitch = 2 * D + 16;           // bytes: rows start in other banks
+    static constexpr int kHeadFloats = static_cast<int>(part_floats(kRows, D));
+    static constexpr int64_t kPartFloats = static_cast<int64_t>(kHeads) * kHeadFloats;
 };
 
-template <int D, int NT>
+template <int D, int NT, int T>
 struct Shared {
-    using S = Shape<D, NT>;
-    alignas(128) uint8_t ring[kWarps][S::kStages][4 * S::kTile];   // K, K, V, V
-    alignas(16) float4 sums[kWarps][S::kMTiles * NT][32];
-    alignas(16) uint8_t q[2][S::kRows][S::kQPitch];
-    alignas(8) uint64_t full[kWarps][S::kStages];
-    uint64_t empty[kWarps][S::kStages];
+    using S = Shape<D, NT, T>;
+    alignas(128) uint8_t ring[S::kStages][4 * kWarps * S::kTile];
+    // the query rows as they are, then in place as matrix operands
+    alignas(16) uint8_t q[2][S::kHeads][S::kRows][S::kQPitch];
+    // what the other warps of a head leave for the one that finishes it
+    alignas(16) float4 sums[T > 1 ? kWarps : 1][T > 1 ? T - 1 : 1][T > 1 ? S::kOwn * NT : 1][T > 1 ? 32 : 1];
+    alignas(8) uint64_t full[S::kStages];
+    uint64_t empty[S::kStages];
     uint64_t item_full[2];
     uint64_t item_empty[2];
     Item item[2];
@@ -178,222 +200,277 @@ struct Shared {
     PlanShared<kWarps + 1> plan;
 };
 
+// Where tile m (0, 1: K; 2, 3: V) of a head's step lies in a stage: heads side
+// by side when a page is one tile, else the two tiles of a head.
+template <int D, int NT, int T>
+__device__ __forceinline__ int32_t stage_at(bool by_tile, int32_t step, int32_t m, int32_t head) {
+    using S = Shape<D, NT, T>;
+    const int32_t at = by_tile ? (4 * step + m) * S::kHeads + head
+                               : ((2 * step + m / 2) * S::kHeads + head) * 2 + m % 2;
+    return at * S::kTile;
+}
+
 // ---------------------------------------------------------------------------
 // the copying warp
 
-template <int D, int NT>
-__device__ __forceinline__ void copy_items(const Fp4Attention &a, Shared<D, NT> &sm, const Run &run,
-                                           int32_t group, Split *record) {
-    using S = Shape<D, NT>;
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
+
+// Arrives at a barrier when this lane's copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(bar) : "memory");
+}
+
+template <int D, int NT, int T>
+__device__ __forceinline__ void copy_items(const Fp4Attention &a, Shared<D, NT, T> &sm, const Run &run,
+                                           const Division &d, Split *record) {
+    using S = Shape<D, NT, T>;
+    constexpr int kHeads = S::kHeads;
     const int32_t lane = threadIdx.x % 32;
-    // A round of steps is 16 copies: lane = 4 * warp + (K, K, V, V).
-    const int32_t to_warp = lane / 4, which = lane % 4;
-    uint32_t fill = 0;                         // steps issued to this lane's warp
-    uint32_t items = 0;
+    uint32_t stage = 0, lap = 0, items = 0;
+
+    // This lane's copy of a round: some tiles of a step of K or of V.
+    const int32_t tiles = a.pools.tiles;
+    const int32_t shift = (tiles & (tiles - 1)) == 0 ? __ffs(tiles) - 1 : -1;
+    const bool by_tile = tiles == 1, by_pair = tiles % 2 == 0;
+    int32_t step, m, head, copies;       // m: its first tile, as in stage_at
+    if (by_tile) {                       // one tile of all heads
+        copies = 4 * T;
+        step = lane / 4, m = lane % 4, head = 0;
+    } else if (by_pair) {                // two tiles of one head
+        copies = 2 * kWarps;
+        step = lane / (2 * kHeads), m = 2 * (lane / kHeads % 2), head = lane % kHeads;
+    } else {                             // one tile of one head
+        copies = 4 * kWarps;
+        step = lane / (4 * kHeads), m = lane / kHeads % 4, head = lane % kHeads;
+    }
+    const uint8_t *pool = m < 2 ? a.pools.k : a.pools.v;
+
     Walk walk;
-    walk.begin(a, run, group, S::kRows);
+    walk.begin(a, d, run);
     for (;;) {
-        const Tile x = tile_of(walk.s, walk.rt, group, S::kRows, a.window);
+        const Tile x = tile_of(walk.s, d, walk.rt);
         const int64_t unit0 = walk.start + kItemCost;
         if (unit0 >= run.end) break;
         const int32_t r0 = static_cast<int32_t>(max(int64_t{0}, run.at - unit0));
         const int32_t r1 = static_cast<int32_t>(min(static_cast<int64_t>(x.units), run.end - unit0));
         if (r1 > r0) {
             Item it;
-            it.begin = x.begin + r0 * kUnit;
-            it.end = min(x.end, x.begin + r1 * kUnit);
+            it.begin = x.begin + r0 * S::kUnit;
+            it.end = min(x.end, x.begin + r1 * S::kUnit);
             it.first = x.first;
-            it.steps = it.end > it.begin ? (it.end - it.begin + kStep - 1) / kStep : 0;
+            it.rounds = it.end > it.begin ? (it.end - it.begin + S::kUnit - 1) / S::kUnit : 0;
             it.ahead = walk.s.length - walk.s.news;
             it.token0 = walk.s.token0;
             it.row0 = x.row0;
             it.rows = x.rows;
-            it.head = walk.head;
+            it.set = walk.set;
             it.part = r0 == 0 && r1 == x.units ? -1 : r0 == 0 ? 1 : 0;
+
+            const int32_t *table = a.block_table + static_cast<int64_t>(walk.seq) * a.table_stride;
+            // The first of this lane's tiles that holds a seen token, its page
+            // and its place in the page; no page: nothing to copy.
+            struct Place { int32_t tile, count; int64_t page; };
+            auto look_up = [&](int32_t at) {
+                Place p;
+                const int32_t lo = max(at + 32 * step + 16 * (m % 2), it.first & ~15);
+                const int32_t hi = min(it.end, at + 32 * step + 16 * (by_pair ? 2 : m % 2 + 1));
+                p.count = lane < copies && lo < hi ? (hi - lo + 15) / 16 : 0;
+                p.tile = 0;
+                p.page = 0;
+                if (p.count > 0) {
+                    const int32_t at16 = lo / 16;
+                    const int32_t page_at = shift >= 0 ? at16 >> shift : at16 / tiles;
+                    p.tile = at16 - page_at * tiles;
+                    p.page = table[page_at];
+                }
+                return p;
+            };
+            Place now = look_up(it.begin);
 
             const uint32_t slot = items % 2;
             if (items >= 2) barrier_wait(smem_addr(&sm.item_empty[slot]), (items / 2 - 1) & 1, &sm.gave_up);
-            const uint32_t bar = smem_addr(&sm.item_full[slot]);
             if (lane == 0) {
                 sm.item[slot] = it;
-                barrier_expect(bar, x.rows * 2 * D);
                 if (it.part == 1) {
                     record->token0 = it.token0;
                     record->row0 = it.row0;
                     record->rows = it.rows;
-                    record->head = it.head;
+                    record->set = it.set;
                     record->blocks = static_cast<int32_t>((unit0 + x.units - 1) / run.per_block) - blockIdx.x + 1;
                 }
             }
-            __syncwarp();
-            if (lane < x.rows) {
-                const int32_t row = x.row0 + lane, qi = row / group;
+            constexpr int kPieces = D / 8;     // of a row
+            for (int32_t i = lane; i < kHeads * x.rows * kPieces; i += 32) {
+                const int32_t r = i / kPieces, h = r / x.rows, row = x.row0 + r - h * x.rows;
+                const int32_t qi = walk.s.news > 1 ? row / d.group : 0;
                 const uint16_t *src = a.q + (it.token0 + qi) * a.q_stride +
-                    (static_cast<int64_t>(it.head) * group + (row - qi * group)) * D;
-                copy_async(smem_addr(sm.q[slot][lane]), src, 2 * D, bar);
+                    ((static_cast<int64_t>(it.set) * kHeads + h) * d.group + (row - qi * d.group)) * D;
+                copy16_async(smem_addr(sm.q[slot][h][row - x.row0]) + 16 * (i % kPieces), src + 8 * (i % kPieces));
             }
+            copies_arrive(smem_addr(&sm.item_full[slot]));
+            if (lane == 0) barrier_arrive(smem_addr(&sm.item_full[slot]));
             ++items;
 
-            const int32_t *table = a.block_table + static_cast<int64_t>(walk.seq) * a.table_stride;
-            const int32_t rounds = (it.steps + kWarps - 1) / kWarps;
-            int32_t at = it.begin + to_warp * kStep;           // this lane's step
-            auto look_up = [&](int32_t tok, int32_t *tile) -> int64_t {
-                if (lane >= 4 * kWarps || tok >= it.end) return 0;
-                *tile = tok / 16;
-                const int32_t page_at = *tile / a.pools.tiles;
-                *tile -= page_at * a.pools.tiles;
-                return table[page_at];
-            };
-            int32_t tile = 0;
-            int64_t page = look_up(at + 16 * (which & 1), &tile);
-            for (int32_t r = 0; r < rounds; ++r) {
-                int32_t tile_next = 0;
-                const int64_t page_next = look_up(at + kUnit + 16 * (which & 1), &tile_next);
-                if (lane < 4 * kWarps && at < it.end) {
-                    const uint32_t stage = fill % S::kStages;
-                    const uint32_t full = smem_addr(&sm.full[to_warp][stage]);
-                    if (fill >= S::kStages)
-                        barrier_wait(smem_addr(&sm.empty[to_warp][stage]), (fill / S::kStages - 1) & 1, &sm.gave_up);
-                    if (which == 0) barrier_expect(full, (it.end - at > 16 ? 4 : 2) * S::kTile);
-                    if (at + 16 * (which & 1) < it.end) {
-                        if (page < 0 || page >= a.pools.num_blocks) {
-                            atomicOr(&g_fp4_attention_error, kFp4ErrSlot);
-                            page = 0;
-                        }
-                        const uint8_t *src = (which < 2 ? a.pools.k : a.pools.v) + page * a.pools.block_stride +
-                            (static_cast<int64_t>(it.head) * a.pools.tiles + tile) * S::kTile;
-                        copy_async(smem_addr(sm.ring[to_warp][stage]) + which * S::kTile, src, S::kTile, full);
-                    }
-                    ++fill;
+            int32_t at = it.begin;
+            for (int32_t r = 0; r < it.rounds; ++r, at += S::kUnit) {
+                const Place next = look_up(at + S::kUnit);
+                const uint32_t full = smem_addr(&sm.full[stage]);
+                if (lap > 0) barrier_wait(smem_addr(&sm.empty[stage]), (lap - 1) & 1, &sm.gave_up);
+                if (lane == 0) {
+                    const int32_t lo = max(at, it.first & ~15), hi = min(it.end, at + S::kUnit);
+                    barrier_expect(full, (hi > lo ? (hi - lo + 15) / 16 : 0) * 2 * kHeads * S::kTile);
                 }
                 __syncwarp();
-                at += kUnit;
-                page = page_next;
-                tile = tile_next;
+                if (now.count > 0) {
+                    if (now.page < 0 || now.page >= a.pools.num_blocks) {
+                        atomicOr(&g_fp4_attention_error, kFp4ErrSlot);
+                        now.page = 0;
+                    }
+                    const uint8_t *src = pool + now.page * a.pools.block_stride +
+                        ((static_cast<int64_t>(it.set) * kHeads + head) * tiles + now.tile) * S::kTile;
+                    // a pair that starts with its second tile
+                    const int32_t skip = by_pair ? now.tile % 2 : 0;
+                    const uint32_t dst = smem_addr(sm.ring[stage]) +
+                        stage_at<D, NT, T>(by_tile, step, m, head) + skip * S::kTile;
+                    copy_async(dst, src, now.count * (by_tile ? kHeads : 1) * S::kTile, full);
+                }
+                if (++stage == S::kStages) stage = 0, ++lap;
+                now = next;
             }
         }
-        if (!walk.next(a, x.units + kItemCost, group, S::kRows)) break;
+        if (!walk.next(a, d, x.units + kItemCost)) break;
     }
     const uint32_t slot = items % 2;
     if (items >= 2) barrier_wait(smem_addr(&sm.item_empty[slot]), (items / 2 - 1) & 1, &sm.gave_up);
-    if (lane == 0) {
-        sm.item[slot].steps = -1;
-        barrier_arrive(smem_addr(&sm.item_full[slot]));
-    }
+    if (lane == 0) sm.item[slot].rounds = -1;
+    copies_arrive(smem_addr(&sm.item_full[slot]));
+    if (lane == 0) barrier_arrive(smem_addr(&sm.item_full[slot]));
 }
 
 // ---------------------------------------------------------------------------
 // the computing warps
 
-// The query rows as the right operand of S^T, and what each column needs.
-template <int D, int NT>
-struct Rows {
-    uint32_t q[NT][D / 16][2];
-    float c[NT][2];                        // factor of raw scores: log2 of a weight
-    int32_t see_hi[NT][2], see_lo[NT][2];  // tokens the column sees
-};
-
-template <int D, int NT>
-__device__ __forceinline__ void load_rows(const Fp4Attention &a, const Item &it,
-                                          const uint8_t (&q)[8 * NT][Shape<D, NT>::kQPitch],
-                                          int32_t group, float k_scale, Rows<D, NT> &r) {
-    const int32_t lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+// Turns a head's query rows into the right operand of S^T, in place, each of
+// its T warps a share, and finds the factors that turn raw scores of this
+// lane's columns into the log2 of a weight.
+template <int D, int NT, int T>
+__device__ __forceinline__ void prepare_rows(const Fp4Attention &a, int32_t rows, uint8_t *q, float k_scale,
+                                             float (&c)[NT][2]) {
+    using S = Shape<D, NT, T>;
+    const int32_t share = threadIdx.x / 32 % T, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+    static_assert(NT * (D / 32) * 512 <= S::kRows * S::kQPitch, "the operands fit where the rows were");
+    uint4 x[NT][D / 32];                   // dimensions [t D/4, (t + 1) D/4) of row g
+    float scale[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const bool live = n * 8 + g < it.rows;
-        uint32_t w[D / 8];
+        const bool live = n * 8 + g < rows;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (live) x = *reinterpret_cast<const uint4 *>(q[n * 8 + g] + t * (D / 2) + 16 * i);
-            w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+            x[n][i] = make_uint4(0, 0, 0, 0);
+            if (live)
+                x[n][i] = *reinterpret_cast<const uint4 *>(q + (n * 8 + g) * S::kQPitch + t * (D / 2) + 16 * i);
         }
         uint32_t most = 0;                 // largest magnitude pattern
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-            most = max(most, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+        for (int i = 0; i < D / 32; ++i) {
+            const uint32_t w[4] = {x[n][i].x, x[n][i].y, x[n][i].z, x[n][i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                most = max(most, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+        }
         most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
         most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
         const int32_t up = min(8 - (static_cast<int32_t>(most >> 7) - 127), 120);
-        const float scale = __int_as_float((127 + up) << 23);
+        scale[n] = __int_as_float((127 + up) << 23);
         const float back = __int_as_float((127 - up) << 23);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-            r.q[n][i][0] = f16x2_of(bf16_low(w[2 * i]) * scale, bf16_high(w[2 * i]) * scale);
-            r.q[n][i][1] = f16x2_of(bf16_low(w[2 * i + 1]) * scale, bf16_high(w[2 * i + 1]) * scale);
-        }
         // A factor above zero keeps masked scores at -infinity; raw scores are
         // below 2^30, so one this small stands for zero.
-        const float mine_c = fmaxf(a.softmax_scale * kLog2e * k_scale * back, 0x1p-100f);
+        const float mine = fmaxf(a.softmax_scale * kLog2e * k_scale * back, 0x1p-100f);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            r.c[n][j] = __shfl_sync(0xFFFFFFFFu, mine_c, 4 * (2 * t + j));
-            const int32_t col = n * 8 + 2 * t + j;
-            const int32_t ci = (it.row0 + min(col, it.rows - 1)) / group;
-            r.see_hi[n][j] = min(it.end, it.ahead + ci + 1);
-            r.see_lo[n][j] = a.window > 0 ? max(0, it.ahead + ci + 1 - a.window) : 0;
-        }
+        for (int j = 0; j < 2; ++j) c[n][j] = __shfl_sync(0xFFFFFFFFu, mine, 4 * (2 * t + j));
     }
-}
-
-// Raw scores of 16 tokens: S^T = K Q^T.
-template <int D, int NT>
-__device__ __forceinline__ void score_tile(const uint8_t *kt, const Rows<D, NT> &r, float (&sc)[NT][4]) {
-    const int32_t lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-    const int32_t tok = 4 * (g / 2) + (g % 2);     // this lane's rows: tok, tok + 2
-    constexpr int kWords = D / 32;                 // code words of a lane's part of a row
-    uint32_t ca[kWords], cb[kWords], za[(D + 127) / 128], zb[(D + 127) / 128];
-    const uint8_t *ra = kt + tok * (D / 2) + t * (D / 8);
-    const uint8_t *rb = ra + D;
-    const uint8_t *sa = kt + 8 * D + tok * (D / 16) + t * (D / 64);
-    const uint8_t *sb = sa + D / 8;
-    if constexpr (D == 64) {
-        const uint2 x = *reinterpret_cast<const uint2 *>(ra);
-        const uint2 y = *reinterpret_cast<const uint2 *>(rb);
-        ca[0] = x.x, ca[1] = x.y, cb[0] = y.x, cb[1] = y.y;
-        za[0] = *sa, zb[0] = *sb;
-    } else {
-#pragma unroll
-        for (int i = 0; i < kWords / 4; ++i) {
-            const uint4 x = reinterpret_cast<const uint4 *>(ra)[i];
-            const uint4 y = reinterpret_cast<const uint4 *>(rb)[i];
-            ca[4 * i] = x.x, ca[4 * i + 1] = x.y, ca[4 * i + 2] = x.z, ca[4 * i + 3] = x.w;
-            cb[4 * i] = y.x, cb[4 * i + 1] = y.y, cb[4 * i + 2] = y.z, cb[4 * i + 3] = y.w;
-        }
-#pragma unroll
-        for (int i = 0; i < D / 128; ++i) {
-            za[i] = reinterpret_cast<const uint16_t *>(sa)[i];
-            zb[i] = reinterpret_cast<const uint16_t *>(sb)[i];
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < (D + 127) / 128; ++i) za[i] = f16x2_of_e4m3x2(za[i]), zb[i] = f16x2_of_e4m3x2(zb[i]);
+    if (T > 1) meet();                     // every warp has read the rows
+    else __syncwarp();
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sc[n][j] = 0.0f;
+        for (int i = 0; i < D / 32; ++i)
+            if (i % T == share)
+                reinterpret_cast<uint4 *>(q)[(i * NT + n) * 32 + lane] = make_uint4(
+                    f16x2_of(bf16_low(x[n][i].x) * scale[n], bf16_high(x[n][i].x) * scale[n]),
+                    f16x2_of(bf16_low(x[n][i].y) * scale[n], bf16_high(x[n][i].y) * scale[n]),
+                    f16x2_of(bf16_low(x[n][i].z) * scale[n], bf16_high(x[n][i].z) * scale[n]),
+                    f16x2_of(bf16_low(x[n][i].w) * scale[n], bf16_high(x[n][i].w) * scale[n]));
+    if (T > 1) meet();
+    else __syncwarp();
+}
+
+// Raw scores of 32 tokens: S^T = K Q^T.
+template <int D, int NT>
+__device__ __forceinline__ void score_step(const uint8_t *tile0, const uint8_t *tile1, const uint4 *rows,
+                                           float (&sc)[2][NT][4]) {
+    const int32_t lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+    const int32_t tok = 4 * (g / 2) + (g % 2);     // this lane's rows of a tile: tok, tok + 2
+    constexpr int kWords = D / 32;                 // code words of a lane's part of a row
+    constexpr int kPairs = (D + 127) / 128;        // pairs of block scales
+    uint32_t ca[2][kWords], cb[2][kWords], za[2][kPairs], zb[2][kPairs];
 #pragma unroll
-    for (int blk = 0; blk < D / 64; ++blk) {       // 16 dimensions, four k-steps
-        const uint32_t s_a = blk % 2 ? high_twice(za[blk / 2]) : low_twice(za[blk / 2]);
-        const uint32_t s_b = blk % 2 ? high_twice(zb[blk / 2]) : low_twice(zb[blk / 2]);
+    for (int m = 0; m < 2; ++m) {
+        const uint8_t *kt = m ? tile1 : tile0;
+        const uint8_t *ra = kt + tok * (D / 2) + t * (D / 8);
+        const uint8_t *rb = ra + D;
+        const uint8_t *sa = kt + 8 * D + tok * (D / 16) + t * (D / 64);
+        const uint8_t *sb = sa + D / 8;
+        if constexpr (D == 64) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(ra);
+            const uint2 y = *reinterpret_cast<const uint2 *>(rb);
+            ca[m][0] = x.x, ca[m][1] = x.y, cb[m][0] = y.x, cb[m][1] = y.y;
+            za[m][0] = *sa, zb[m][0] = *sb;
+        } else {
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 x = reinterpret_cast<const uint4 *>(ra)[i];
+                const uint4 y = reinterpret_cast<const uint4 *>(rb)[i];
+                ca[m][4 * i] = x.x, ca[m][4 * i + 1] = x.y, ca[m][4 * i + 2] = x.z, ca[m][4 * i + 3] = x.w;
+                cb[m][4 * i] = y.x, cb[m][4 * i + 1] = y.y, cb[m][4 * i + 2] = y.z, cb[m][4 * i + 3] = y.w;
+            }
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) {
+                za[m][i] = reinterpret_cast<const uint16_t *>(sa)[i];
+                zb[m][i] = reinterpret_cast<const uint16_t *>(sb)[i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i)
+            za[m][i] = f16x2_of_e4m3x2(za[m][i]), zb[m][i] = f16x2_of_e4m3x2(zb[m][i]);
+    }
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {             // eight dimensions of each lane, two k-steps
+        uint4 q[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) q[n] = rows[(w * NT + n) * 32 + lane];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            const uint32_t s_a = w / 2 % 2 ? high_twice(za[m][w / 4]) : low_twice(za[m][w / 4]);
+            const uint32_t s_b = w / 2 % 2 ? high_twice(zb[m][w / 4]) : low_twice(zb[m][w / 4]);
             uint32_t xa[4], xb[4];
-            f16x2_of_e2m1x8(ca[2 * blk + w], xa);
-            f16x2_of_e2m1x8(cb[2 * blk + w], xb);
+            f16x2_of_e2m1x8(ca[m][w], xa);
+            f16x2_of_e2m1x8(cb[m][w], xb);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 xa[i] = mul_f16x2(xa[i], s_a);
                 xb[i] = mul_f16x2(xb[i], s_b);
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const int ks = 4 * blk + 2 * w + i;
-                    mma(sc[n], xa[2 * i], xb[2 * i], xa[2 * i + 1], xb[2 * i + 1], r.q[n][ks][0],
-                        r.q[n][ks][1]);
-                }
+            for (int n = 0; n < NT; ++n) {
+                if (w == 0)
+                    mma_first(sc[m][n], xa[0], xb[0], xa[1], xb[1], q[n].x, q[n].y);
+                else
+                    mma(sc[m][n], xa[0], xb[0], xa[1], xb[1], q[n].x, q[n].y);
+                mma(sc[m][n], xa[2], xb[2], xa[3], xb[3], q[n].z, q[n].w);
+            }
         }
     }
 }
@@ -455,30 +532,37 @@ __device__ __forceinline__ float row_lse(float most, float l) {
     return l == 0.0f ? -INFINITY : kLn2 * (most + (log2f(l) - kShift));
 }
 
-// A pair of dimensions of one row, rounded and stored.
-__device__ __forceinline__ void store_pair(const Fp4Attention &a, int32_t token, int32_t q_head,
-                                           int32_t dim, int32_t at, float x, float y) {
-    *reinterpret_cast<uint32_t *>(a.out + token * a.out_stride + static_cast<int64_t>(q_head) * dim + at) =
-        bf16x2_of(x, y);
+// The place of a row of an item in `out` and `lse`.
+struct RowPlace {
+    int32_t token, q_head;
+};
+__device__ __forceinline__ RowPlace row_place(int32_t token0, int32_t row, int32_t head, int32_t group) {
+    const int32_t qi = row / group;
+    return {token0 + qi, head * group + (row - qi * group)};
 }
 
-template <int D, int NT>
-__device__ __forceinline__ void compute_items(const Fp4Attention &a, Shared<D, NT> &sm, int32_t group,
+template <int D, int NT, int T>
+__device__ __forceinline__ void compute_items(const Fp4Attention &a, Shared<D, NT, T> &sm, const Division &d,
                                               float k_scale, float v_scale) {
-    using S = Shape<D, NT>;
+    using S = Shape<D, NT, T>;
     const int32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int32_t hh = warp / T, step = warp % T;  // this warp's head, and its steps of a round
     const int32_t g = lane / 4, t = lane % 4;
     const int32_t tok_a = 4 * (g / 2) + (g % 2);   // this lane's score rows: tok_a, tok_a + 2
-    uint32_t drain = 0;                            // steps this warp has used
+    const bool by_tile = a.pools.tiles == 1;
+    int32_t place[4];                              // of its tiles in a stage
+#pragma unroll
+    for (int m = 0; m < 4; ++m) place[m] = stage_at<D, NT, T>(by_tile, step, m, hh);
+    uint32_t stage = 0, phase = 0;
     for (uint32_t items = 0;; ++items) {
         const uint32_t slot = items % 2;
         barrier_wait(smem_addr(&sm.item_full[slot]), (items / 2) & 1, &sm.gave_up);
-        const Item it = sm.item[slot];
-        if (it.steps < 0) return;
-        const int32_t steps = it.steps > warp ? (it.steps - warp + kWarps - 1) / kWarps : 0;
+        const Item &it = sm.item[slot];
+        if (it.rounds < 0) return;
 
-        Rows<D, NT> r;
-        load_rows<D, NT>(a, it, sm.q[slot], group, k_scale, r);
+        float c[NT][2];
+        prepare_rows<D, NT, T>(a, it.rows, sm.q[slot][hh][0], k_scale, c);
+        const uint4 *rows = reinterpret_cast<const uint4 *>(sm.q[slot][hh][0]);
         float top[NT][2], ref[NT][2], sum[NT][2];  // ref: what scores are taken against
         float o[S::kMTiles][NT][4];
 #pragma unroll
@@ -490,30 +574,36 @@ __device__ __forceinline__ void compute_items(const Fp4Attention &a, Shared<D, N
 #pragma unroll
                 for (int j = 0; j < 4; ++j) o[i][n][j] = 0.0f;
         }
-        const int32_t all_hi = min(it.end, it.ahead + it.row0 / group + 1);   // every row sees below
+        // every row sees the tokens in [all_lo, all_hi)
+        const int32_t all_hi = min(it.end, it.ahead + it.row0 / d.group + 1);
         const int32_t all_lo =
-            a.window > 0 ? max(0, it.ahead + (it.row0 + it.rows - 1) / group + 1 - a.window) : 0;
+            a.window > 0 ? max(0, it.ahead + (it.row0 + it.rows - 1) / d.group + 1 - a.window) : 0;
+        int32_t at = it.begin + step * kStep;
+        const int32_t rounds = it.rounds;
 
-        for (int32_t k = 0; k < steps; ++k) {
-            const int32_t at = it.begin + (warp + k * kWarps) * kStep;
-            const uint32_t stage = drain % S::kStages;
-            barrier_wait(smem_addr(&sm.full[warp][stage]), (drain / S::kStages) & 1, &sm.gave_up);
-            const uint8_t *ring = sm.ring[warp][stage];
+        for (int32_t r = 0; r < rounds; ++r, at += S::kUnit) {
+            barrier_wait(smem_addr(&sm.full[stage]), phase, &sm.gave_up);
+            const uint8_t *ring = sm.ring[stage];
             const bool edge = at + kStep > all_hi || at < all_lo;
+            if (T == 1 || at < it.end) {
 
             float sc[2][NT][4];
-#pragma unroll
-            for (int m = 0; m < 2; ++m) score_tile<D, NT>(ring + m * S::kTile, r, sc[m]);
+            score_step<D, NT>(ring + place[0], ring + place[1], rows, sc);
             if (edge) {
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                    for (int j = 0; j < 2; ++j) {
+                        const int32_t ci = it.ahead + (it.row0 + min(n * 8 + 2 * t + j, it.rows - 1)) / d.group + 1;
+                        const int32_t hi = min(it.end, ci), lo = a.window > 0 ? ci - a.window : 0;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int32_t tok = at + 16 * m + tok_a + 2 * (j / 2);
-                            if (tok >= r.see_hi[n][j % 2] || tok < r.see_lo[n][j % 2]) sc[m][n][j] = -INFINITY;
-                        }
+                        for (int m = 0; m < 2; ++m)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int32_t tok = at + 16 * m + tok_a + 2 * h;
+                                if (tok >= hi || tok < lo) sc[m][n][2 * h + j] = -INFINITY;
+                            }
+                    }
             }
 
             // ---- running maximum and sum -------------------------------------
@@ -523,7 +613,7 @@ __device__ __forceinline__ void compute_items(const Fp4Attention &a, Shared<D, N
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    mx[n][j] = r.c[n][j] * fmaxf(fmaxf(sc[0][n][j], sc[0][n][2 + j]),
+                    mx[n][j] = c[n][j] * fmaxf(fmaxf(sc[0][n][j], sc[0][n][2 + j]),
                                                  fmaxf(sc[1][n][j], sc[1][n][2 + j]));
                     grew |= mx[n][j] > top[n][j];
                 }
@@ -559,7 +649,7 @@ __device__ __forceinline__ void compute_items(const Fp4Attention &a, Shared<D, N
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         float &x = sc[m][n][j];
-                        x = exp2_fast(fmaf(x, r.c[n][j % 2], -ref[n][j % 2]));
+                        x = exp2_fast(fmaf(x, c[n][j % 2], -ref[n][j % 2]));
                         sum[n][j % 2] += x;
                     }
 #pragma unroll
@@ -571,117 +661,155 @@ __device__ __forceinline__ void compute_items(const Fp4Attention &a, Shared<D, N
             if (edge) {
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
-                    add_tile<D, NT, true>(ring + (2 + m) * S::kTile, it.first - (at + 16 * m),
+                    add_tile<D, NT, true>(ring + place[2 + m], it.first - (at + 16 * m),
                                           it.end - (at + 16 * m), pf[m], o);
             } else {
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
-                    add_tile<D, NT, false>(ring + (2 + m) * S::kTile, 0, 16, pf[m], o);
+                    add_tile<D, NT, false>(ring + place[2 + m], 0, 16, pf[m], o);
             }
-            ++drain;
+            }
             __syncwarp();                      // every lane has read the stage
-            if (lane == 0) barrier_arrive(smem_addr(&sm.empty[warp][stage]));
+            if (lane == 0) barrier_arrive(smem_addr(&sm.empty[stage]));
+            if (++stage == S::kStages) stage = 0, phase ^= 1;
         }
 
-        // ---- join the warps ---------------------------------------------------
-        const int32_t busy = min(kWarps, max(1, it.steps));    // warps that had a step
-        if (warp < busy) {
+        // ---- join the warps of a head -------------------------------------------
+        const int32_t busy = min(T, max(1, (it.end - it.begin + kStep - 1) / kStep));   // that had a step
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float l = sum[n][j];
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int off = 4; off < 32; off *= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, off);
+                for (int off = 4; off < 32; off *= 2)
+                    sum[n][j] += __shfl_xor_sync(0xFFFFFFFFu, sum[n][j], off);
+        if (T > 1) {
+            if (step < busy) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
                     if (g == 0) {
-                        sm.top[warp][n * 8 + 2 * t + j] = top[n][j];
-                        sm.sum[warp][n * 8 + 2 * t + j] = l;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            sm.top[warp][n * 8 + 2 * t + j] = top[n][j];
+                            sm.sum[warp][n * 8 + 2 * t + j] = sum[n][j];
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < S::kMTiles; ++i) {
+                        const int owner = i / S::kOwn;
+                        if (owner != step)
+                            sm.sums[hh * T + owner][step - (step > owner)][i % S::kOwn * NT + n][lane] =
+                                make_float4(o[i][n][0], o[i][n][1], o[i][n][2], o[i][n][3]);
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < S::kMTiles; ++i)
-                    sm.sums[warp][i * NT + n][lane] =
-                        make_float4(o[i][n][0], o[i][n][1], o[i][n][2], o[i][n][3]);
             }
+            meet();
         }
-        meet();
-        // Each warp finishes a quarter of the dimensions.
-        float *part = part_at(a.workspace, 2 * static_cast<int64_t>(blockIdx.x) + max(it.part, 0), S::kRows, D);
+        // Each of its warps finishes a share of the dimensions.
+        const int32_t head = it.set * S::kHeads + hh;
+        float *part = part_at(a.workspace, 2 * static_cast<int64_t>(blockIdx.x) + max(it.part, 0), S::kPartFloats) +
+                      hh * S::kHeadFloats;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float f[kWarps][2], most[2], l[2];
+            float f[T][2], most[2], l[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const int32_t col = n * 8 + 2 * t + j;
-                most[j] = -INFINITY;
-                for (int w = 0; w < busy; ++w) most[j] = fmaxf(most[j], sm.top[w][col]);
-                const float base = most[j] == -INFINITY ? 0.0f : most[j];
-                l[j] = 0.0f;
+                most[j] = top[n][j], l[j] = sum[n][j], f[0][j] = 1.0f;
+                if (T > 1) {
+                    const int32_t col = n * 8 + 2 * t + j;
+                    most[j] = -INFINITY;
+                    for (int w = 0; w < busy; ++w) most[j] = fmaxf(most[j], sm.top[hh * T + w][col]);
+                    const float base = most[j] == -INFINITY ? 0.0f : most[j];
+                    l[j] = 0.0f;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    f[w][j] = w < busy ? exp2_fast(sm.top[w][col] - base) : 0.0f;
-                    if (w < busy) l[j] += f[w][j] * sm.sum[w][col];
+                    for (int w = 0; w < T; ++w) {
+                        f[w][j] = w < busy ? exp2_fast(sm.top[hh * T + w][col] - base) : 0.0f;
+                        if (w < busy) l[j] += f[w][j] * sm.sum[hh * T + w][col];
+                    }
                 }
             }
+            const float inv[2] = {row_factor(l[0], v_scale), row_factor(l[1], v_scale)};
+            uint32_t packed[2][S::kOwn];       // rounded pairs of dimensions, by row
 #pragma unroll
-            for (int ii = 0; ii < S::kMTiles / kWarps; ++ii) {
-                const int i = warp * (S::kMTiles / kWarps) + ii;
-                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int ii = 0; ii < S::kOwn; ++ii) {
+                float x[4];
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w)
-                    if (w < busy) {
-                        const float4 v = sm.sums[w][i * NT + n][lane];
-                        x.x += f[w][0] * v.x, x.y += f[w][1] * v.y;
-                        x.z += f[w][0] * v.z, x.w += f[w][1] * v.w;
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    x[j] = o[ii][n][j];
+#pragma unroll
+                    for (int w = 1; w < T; ++w) x[j] = step == w ? o[w * S::kOwn + ii][n][j] : x[j];
+                }
+                if (T > 1) {
+                    float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int w = 0; w < T; ++w)
+                        if (w < busy) {
+                            const float4 v = w == step ? make_float4(x[0], x[1], x[2], x[3])
+                                                       : sm.sums[warp][w - (w > step)][ii * NT + n][lane];
+                            y[0] += f[w][0] * v.x, y[1] += f[w][1] * v.y;
+                            y[2] += f[w][0] * v.z, y[3] += f[w][1] * v.w;
+                        }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[j] = y[j];
+                }
+                if (it.part >= 0)
+                    reinterpret_cast<float4 *>(part)[((step * S::kOwn + ii) * NT + n) * 32 + lane] =
+                        make_float4(x[0], x[1], x[2], x[3]);
+                packed[0][ii] = bf16x2_of(x[0] * inv[0], x[2] * inv[0]);
+                packed[1][ii] = bf16x2_of(x[1] * inv[1], x[3] * inv[1]);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int32_t row = n * 8 + 2 * t + j;
                 if (it.part >= 0) {
-                    reinterpret_cast<float4 *>(part)[(i * NT + n) * 32 + lane] = x;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int32_t row = n * 8 + 2 * t + j;
-                        if (row >= it.rows) continue;
-                        const int32_t qi = (it.row0 + row) / group;
-                        const float inv = row_factor(l[j], v_scale);
-                        store_pair(a, it.token0 + qi, it.head * group + (it.row0 + row - qi * group), D,
-                                   g * (D / 8) + 2 * i, (j ? x.y : x.x) * inv, (j ? x.w : x.z) * inv);
-                    }
-                }
-            }
-            if (warp == 0 && g == 0) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int32_t row = n * 8 + 2 * t + j;
-                    if (it.part >= 0) {
+                    if (step == 0 && g == 0) {
                         part[S::kRows * D + row] = most[j];
                         part[S::kRows * D + S::kRows + row] = l[j];
-                    } else if (a.lse != nullptr && row < it.rows) {
-                        const int32_t qi = (it.row0 + row) / group;
-                        a.lse[static_cast<int64_t>(it.token0 + qi) * a.q_heads + it.head * group +
-                              (it.row0 + row - qi * group)] = row_lse(most[j], l[j]);
                     }
+                } else if (row < it.rows) {
+                    const RowPlace p = row_place(it.token0, it.row0 + row, head, d.group);
+                    uint16_t *out = a.out + p.token * a.out_stride + static_cast<int64_t>(p.q_head) * D +
+                                    g * (D / 8) + step * S::kOwn * 2;
+                    if constexpr (S::kOwn % 4 == 0) {
+#pragma unroll
+                        for (int i = 0; i < S::kOwn; i += 4)
+                            *reinterpret_cast<uint4 *>(out + 2 * i) = make_uint4(
+                                packed[j][i], packed[j][i + 1], packed[j][i + 2], packed[j][i + 3]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < S::kOwn; ++i) *reinterpret_cast<uint32_t *>(out + 2 * i) = packed[j][i];
+                    }
+                    if (a.lse != nullptr && step == 0 && g == 0)
+                        a.lse[static_cast<int64_t>(p.token) * a.q_heads + p.q_head] = row_lse(most[j], l[j]);
                 }
             }
         }
-        meet();                                // the sums may be written again
+        if (T > 1) meet();                     // the sums may be written again
+        else __syncwarp();
         if (lane == 0) barrier_arrive(smem_addr(&sm.item_empty[slot]));
     }
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) fp4_attention_kernel(const Fp4Attention a) {
-    using S = Shape<D, NT>;
-    extern __shared__ __align__(128) uint8_t smem_raw[];
-    Shared<D, NT> &sm = *reinterpret_cast<Shared<D, NT> *>(smem_raw);
-    const int32_t group = a.q_heads / a.pools.heads;
+template <int D, int NT, int T>
+__device__ __forceinline__ Division division(const Fp4Attention &a) {
+    using S = Shape<D, NT, T>;
+    return {a.q_heads / a.pools.heads, S::kRows, a.pools.heads / S::kHeads, S::kUnit, a.window};
+}
 
-    if (threadIdx.x < kWarps * S::kStages) {
-        barrier_init(smem_addr(&sm.full[0][0] + threadIdx.x), 1);
-        barrier_init(smem_addr(&sm.empty[0][0] + threadIdx.x), 1);
+template <int D, int NT, int T>
+__global__ void __launch_bounds__(kThreads, (Shape<D, NT, T>::kBlocks)) fp4_attention_kernel(const Fp4Attention a) {
+    using S = Shape<D, NT, T>;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    Shared<D, NT, T> &sm = *reinterpret_cast<Shared<D, NT, T> *>(smem_raw);
+    const Division d = division<D, NT, T>(a);
+
+    if (threadIdx.x < S::kStages) {
+        barrier_init(smem_addr(&sm.full[threadIdx.x]), 1);
+        barrier_init(smem_addr(&sm.empty[threadIdx.x]), kWarps);
     }
     if (threadIdx.x == 0) sm.gave_up = 0;
     if (threadIdx.x < 2) {
-        barrier_init(smem_addr(&sm.item_full[threadIdx.x]), 1);
+        barrier_init(smem_addr(&sm.item_full[threadIdx.x]), 33);   // the copying lanes, and the item itself
         barrier_init(smem_addr(&sm.item_empty[threadIdx.x]), kWarps);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -696,93 +824,123 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) fp4_attention
         if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_fp4_attention_error, kFp4ErrScale);
         return;
     }
-    const Run run = block_run<kWarps + 1>(a, group, S::kRows, &g_fp4_attention_error, sm.plan);
+    const Run run = block_run<kWarps + 1>(a, d, &g_fp4_attention_error, sm.plan);
     if (run.at >= run.end) return;             // the whole block
     if (threadIdx.x >= 32 * kWarps)
-        copy_items<D, NT>(a, sm, run, group, record);
+        copy_items<D, NT, T>(a, sm, run, d, record);
     else
-        compute_items<D, NT>(a, sm, group, k_scale, v_scale);
+        compute_items<D, NT, T>(a, sm, d, k_scale, v_scale);
     if (*static_cast<volatile uint32_t *>(&sm.gave_up)) __nanosleep(1000000);   // copies under way land
 }
 
 // ---------------------------------------------------------------------------
 // the join
 
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 16;         // at most, of a block
 
-// Block (c, y) merges some dimensions of the item that began in block c:
-// `units` of the 32-lane, 4-value fragments its parts are stored in, eight or
-// fewer, its warps shared out over the parts where there are fewer.
-template <int D, int NT>
-__global__ void __launch_bounds__(32 * kJoinWarps) fp4_attention_join_kernel(const Fp4Attention a,
-                                                                             int32_t units) {
-    using S = Shape<D, NT>;
+// Block (c, y) merges some dimensions of one head of the item that began in
+// block c, or with few items of the c-th item that is split: `units` of the
+// 32-lane, 4-value fragments its parts are stored in, a warp each, and where
+// it has more warps its parts are dealt out over them.  The parts are met once,
+// with a running maximum like the tokens were, four of them under way at a time:
+// more cost registers, and with them the blocks that run side by side.
+template <int D, int NT, int T>
+__global__ void __launch_bounds__(32 * kJoinWarps, 2) fp4_attention_join_kernel(const Fp4Attention a,
+                                                                             int32_t units,
+                                                                             int32_t search) {
+    using S = Shape<D, NT, T>;
     constexpr int kRows = S::kRows;
-    __shared__ float weight[kMaxBlocks][kRows];    // 2^(top of the part - top)
-    __shared__ float most_of[kRows], sum_of[kRows];
-    __shared__ float4 share[kJoinWarps][32];
+    constexpr int kBatch = 4;
+    __shared__ float4 share_x[kJoinWarps][32];
+    __shared__ float4 share_l[kJoinWarps][32];     // tops and sums of the two rows
+    __shared__ int32_t found;
     pdl_wait();
     pdl_allow_next();
-    const int32_t c = blockIdx.x;
-    const Split s = static_cast<const Split *>(a.workspace)[c];
+    const Split *records = static_cast<const Split *>(a.workspace);
+    const int32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    int32_t c = blockIdx.x;
+    if (search > 0) {                              // in the records of so many blocks
+        if (threadIdx.x == 0) found = -1;
+        __syncthreads();
+        if (warp == 0) {
+            int32_t before = 0;
+            for (int32_t first = 0; first < search && before <= c; first += 32) {
+                const bool split = first + lane < search && records[first + lane].blocks > 0;
+                const uint32_t those = __ballot_sync(0xFFFFFFFFu, split);
+                if (split && before + __popc(those & ((1u << lane) - 1)) == c) found = first + lane;
+                before += __popc(those);
+            }
+        }
+        __syncthreads();
+        if (found < 0) return;
+        c = found;
+    }
+    const Split s = records[c];
     if (s.blocks == 0) return;
     float k_scale, v_scale;
     load_scales(a, &k_scale, &v_scale);
-    // part 1 of block c, then part 0 of the blocks behind it
-    auto part = [&](int32_t i) -> const float * {
-        return part_at(a.workspace, 2 * static_cast<int64_t>(c + i) + (i == 0 ? 1 : 0), kRows, D);
-    };
-    const int32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    for (int32_t row = warp; row < kRows; row += kJoinWarps) {
-        float most = -INFINITY;
-        for (int32_t i = lane; i < s.blocks; i += 32) {
-            weight[i][row] = part(i)[kRows * D + row];
-            most = fmaxf(most, weight[i][row]);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o /= 2) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-        const float base = most == -INFINITY ? 0.0f : most;
-        float l = 0.0f;
-        for (int32_t i = lane; i < s.blocks; i += 32) {
-            const float f = exp2_fast(weight[i][row] - base);
-            weight[i][row] = f;
-            l += f * part(i)[kRows * D + kRows + row];
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o /= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-        if (lane == 0) most_of[row] = most, sum_of[row] = l;
-    }
-    __syncthreads();
-    const int32_t groups = kJoinWarps / units, which = warp / units;
-    const int32_t unit = blockIdx.y * units + warp % units;        // i * NT + n
+    const int32_t slices = S::kMTiles * NT / units;                // of a head
+    const int32_t hh = blockIdx.y / slices;
+    const int32_t groups = blockDim.x / 32 / units, which = warp / units;
+    const int32_t unit = (blockIdx.y % slices) * units + warp % units;   // i * NT + n
     const int32_t col = (unit % NT) * 8 + 2 * (lane % 4);
-    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-    for (int32_t i = which; i < s.blocks; i += groups) {
-        const float4 v = reinterpret_cast<const float4 *>(part(i))[unit * 32 + lane];
-        const float f0 = weight[i][col], f1 = weight[i][col + 1];
-        x.x += f0 * v.x, x.y += f1 * v.y, x.z += f0 * v.z, x.w += f1 * v.w;
+    float top[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto meet_one = [&](const float (&t)[2], const float (&n)[2], const float (&v)[4]) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float now = fmaxf(top[j], t[j]);
+            const float base = now == -INFINITY ? 0.0f : now;
+            const float f = exp2_fast(top[j] - base), e = exp2_fast(t[j] - base);
+            top[j] = now;
+            l[j] = l[j] * f + n[j] * e;
+            x[j] = x[j] * f + v[j] * e;
+            x[2 + j] = x[2 + j] * f + v[2 + j] * e;
+        }
+    };
+    for (int32_t i0 = which; i0 < s.blocks; i0 += groups * kBatch) {
+        float2 t[kBatch], n[kBatch];
+        float4 v[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int32_t i = i0 + k * groups;
+            t[k] = make_float2(-INFINITY, -INFINITY), n[k] = make_float2(0.0f, 0.0f);
+            v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (i < s.blocks) {
+                // part 1 of block c, then part 0 of the blocks behind it
+                const float *p = part_at(a.workspace, 2 * static_cast<int64_t>(c + i) + (i == 0 ? 1 : 0),
+                                         S::kPartFloats) + hh * S::kHeadFloats;
+                t[k] = *reinterpret_cast<const float2 *>(p + kRows * D + col);
+                n[k] = *reinterpret_cast<const float2 *>(p + kRows * D + kRows + col);
+                v[k] = reinterpret_cast<const float4 *>(p)[unit * 32 + lane];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            meet_one({t[k].x, t[k].y}, {n[k].x, n[k].y}, {v[k].x, v[k].y, v[k].z, v[k].w});
     }
-    share[warp][lane] = x;
-    __syncthreads();
-    if (which > 0) return;
-    for (int32_t w = 1; w < groups; ++w) {
-        const float4 v = share[w * units + warp][lane];
-        x.x += v.x, x.y += v.y, x.z += v.z, x.w += v.w;
+    if (groups > 1) {
+        if (which > 0) {
+            share_x[warp][lane] = make_float4(x[0], x[1], x[2], x[3]);
+            share_l[warp][lane] = make_float4(top[0], top[1], l[0], l[1]);
+        }
+        __syncthreads();
+        if (which > 0) return;
+        for (int32_t w = warp + units; w < groups * units; w += units) {
+            const float4 v = share_x[w][lane], m = share_l[w][lane];
+            meet_one({m.x, m.y}, {m.z, m.w}, {v.x, v.y, v.z, v.w});
+        }
     }
-    const int32_t group = a.q_heads / a.pools.heads;
     const int32_t i = unit / NT;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int32_t row = col + j;
         if (row >= s.rows) continue;
-        const int32_t qi = (s.row0 + row) / group;
-        const int32_t q_head = s.head * group + (s.row0 + row - qi * group);
-        const float inv = row_factor(sum_of[row], v_scale);
-        store_pair(a, s.token0 + qi, q_head, D, (lane / 4) * (D / 8) + 2 * i, (j ? x.y : x.x) * inv,
-                   (j ? x.w : x.z) * inv);
+        const RowPlace p = row_place(s.token0, s.row0 + row, s.set * S::kHeads + hh, a.q_heads / a.pools.heads);
+        const float inv = row_factor(l[j], v_scale);
+        *reinterpret_cast<uint32_t *>(a.out + p.token * a.out_stride + static_cast<int64_t>(p.q_head) * D +
+                                      (lane / 4) * (D / 8) + 2 * i) = bf16x2_of(x[j] * inv, x[2 + j] * inv);
         if (a.lse != nullptr && i == 0 && lane < 4)
-            a.lse[static_cast<int64_t>(s.token0 + qi) * a.q_heads + q_head] = row_lse(most_of[row], sum_of[row]);
+            a.lse[static_cast<int64_t>(p.token) * a.q_heads + p.q_head] = row_lse(top[j], l[j]);
     }
 }
 
@@ -797,12 +955,15 @@ int tiles_of(int64_t batch, int64_t num_tokens, int32_t group, int32_t dim) {
     return rows <= 8 || dim == 256 ? 1 : 2;
 }
 
-template <int D, int NT>
+// Warps of a head: a block takes as many of four heads as divide their number.
+int warps_of_head(int32_t kv_heads) { return kv_heads % 4 == 0 ? 1 : kv_heads % 2 == 0 ? 2 : 4; }
+
+template <int D, int NT, int T>
 cudaError_t launch_tiles(const Fp4Attention &a, cudaStream_t stream) {
-    using S = Shape<D, NT>;
-    constexpr size_t kSmem = sizeof(Shared<D, NT>);
+    using S = Shape<D, NT, T>;
+    constexpr size_t kSmem = sizeof(Shared<D, NT, T>);
     static_assert(S::kBlocks * (kSmem + 1024) <= 228 * 1024, "the blocks of an SM fit its shared memory");
-    auto kernel = fp4_attention_kernel<D, NT>;
+    auto kernel = fp4_attention_kernel<D, NT, T>;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -813,19 +974,28 @@ cudaError_t launch_tiles(const Fp4Attention &a, cudaStream_t stream) {
     // No more blocks than there can be points on the axis.
     const int32_t group = a.q_heads / a.pools.heads;
     const int64_t items = ((static_cast<int64_t>(a.num_tokens) * group + S::kRows - 1) / S::kRows + a.batch) *
-                          a.pools.heads;
-    const int64_t longest = (a.table_width * a.pools.tiles * 16 + kUnit - 1) / kUnit + 1 + kItemCost;
+                          (a.pools.heads / S::kHeads);
+    const int64_t longest = a.table_width * a.pools.tiles * 16 / S::kUnit + 2 + kItemCost;
     int64_t grid = static_cast<int64_t>(sms) * S::kBlocks;
-    if (grid > kMaxBlocks) grid = kMaxBlocks;
+    if (grid > kMaxBlocks / 3 * S::kBlocks) grid = kMaxBlocks / 3 * S::kBlocks;
     if (items < grid && items * longest < grid) grid = items * longest;
     e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), kThreads, kSmem, stream, a);
     if (e != cudaSuccess) return e;
-    // Few items have many parts each: their dimensions go to several blocks.
+    // Few items have many parts each: one fragment to a block of 16 warps.
     constexpr int32_t kUnits = S::kMTiles * NT;
-    const int32_t units = items * 8 <= sms ? 1 : kUnits < kJoinWarps ? kUnits : kJoinWarps;
-    return launch_pdl(fp4_attention_join_kernel<D, NT>,
-                      dim3(static_cast<unsigned>(grid), static_cast<unsigned>(kUnits / units)),
-                      32 * kJoinWarps, 0, stream, a, units);
+    const bool few = items * 8 <= sms && items < grid;
+    const int32_t units = few ? 1 : kUnits < 8 ? kUnits : 8;
+    return launch_pdl(fp4_attention_join_kernel<D, NT, T>,
+                      dim3(static_cast<unsigned>(few ? items : grid),
+                           static_cast<unsigned>(S::kHeads * kUnits / units)),
+                      32 * (few ? kJoinWarps : 8), 0, stream, a, units, few ? static_cast<int32_t>(grid) : 0);
+}
+
+template <int D, int NT>
+cudaError_t launch_heads(const Fp4Attention &a, cudaStream_t stream) {
+    const int t = warps_of_head(a.pools.heads);
+    return t == 1 ? launch_tiles<D, NT, 1>(a, stream)
+           : t == 2 ? launch_tiles<D, NT, 2>(a, stream) : launch_tiles<D, NT, 4>(a, stream);
 }
 
 }  // namespace
@@ -833,16 +1003,17 @@ cudaError_t launch_tiles(const Fp4Attention &a, cudaStream_t stream) {
 int64_t fp4_attention_workspace(int64_t batch, int64_t num_tokens, int32_t q_heads,
                                 int32_t kv_heads, int32_t dim) {
     if (batch == 0) return 0;
-    const int nt = tiles_of(batch, num_tokens, q_heads / kv_heads, dim);
-    return kRecordBytes + kMaxBlocks * 2 * 4 * part_floats(8 * nt, dim);
+    const int rows = 8 * tiles_of(batch, num_tokens, q_heads / kv_heads, dim);
+    const int64_t blocks = rows * dim <= 1024 ? kMaxBlocks : kMaxBlocks / 3 * 2;   // as Shape::kBlocks
+    return kRecordBytes + blocks * 2 * 4 * (kWarps / warps_of_head(kv_heads)) * part_floats(rows, dim);
 }
 
 cudaError_t launch_fp4_attention(const Fp4Attention &a, cudaStream_t stream) {
     const int nt = tiles_of(a.batch, a.num_tokens, a.q_heads / a.pools.heads, a.pools.dim);
     switch (a.pools.dim) {
-    case 64: return nt == 1 ? launch_tiles<64, 1>(a, stream) : launch_tiles<64, 2>(a, stream);
-    case 128: return nt == 1 ? launch_tiles<128, 1>(a, stream) : launch_tiles<128, 2>(a, stream);
-    default: return launch_tiles<256, 1>(a, stream);
+    case 64: return nt == 1 ? launch_heads<64, 1>(a, stream) : launch_heads<64, 2>(a, stream);
+    case 128: return nt == 1 ? launch_heads<128, 1>(a, stream) : launch_heads<128, 2>(a, stream);
+    default: return launch_heads<256, 1>(a, stream);
     }
 }
 

@@ -1,9 +1,9 @@
 // How attention over the 4-bit cache is divided among the blocks of a launch.
 //
-// An item is one (sequence, KV head, tile of query rows).  It is made of units
-// of kUnit cached tokens, counted from the first token its own rows see, and
-// costs its units plus kItemCost: loading the rows and finishing the sums take
-// about as long as a unit.  Items are laid side by side on one axis, every
+// An item is one (sequence, set of KV heads, tile of query rows).  It is made
+// of units of some cached tokens, counted from the first token its own rows
+// see, and costs its units plus kItemCost: loading the rows and finishing the
+// sums take about as long as a unit.  Items are laid side by side on one axis, every
 // block takes an equal run of it, and unit j of an item lies at the point
 // item start + kItemCost + j.  A block finds its run from the lengths on the
 // device, so a launch depends on sizes alone and may be captured.
@@ -18,9 +18,17 @@
 namespace fp8q {
 namespace fp4_plan {
 
-constexpr int kUnit = 128;             // cached tokens of a unit
 constexpr int kItemCost = 1;           // units an item costs beside its own
-constexpr int kMaxBlocks = 592;        // blocks a workspace has room for
+constexpr int kMaxBlocks = 444;        // blocks a workspace has room for
+
+// How a kernel divides its work.
+struct Division {
+    int32_t group;       // query heads of a KV head
+    int32_t tile_rows;   // rows of a tile
+    int32_t sets;        // sets of KV heads
+    int32_t unit;        // cached tokens of a unit
+    int32_t window;
+};
 
 // One sequence as the kernels see it: bad lengths and ranges are cut to what
 // the buffers hold and reported.
@@ -31,8 +39,8 @@ struct Sequence {
     int32_t row_tiles;
 };
 
-__device__ __forceinline__ Sequence sequence(const Fp4Attention &a, int32_t b, int32_t group,
-                                             int32_t tile_rows, bool *bad) {
+__device__ __forceinline__ Sequence sequence(const Fp4Attention &a, const Division &d, int32_t b,
+                                             bool *bad) {
     Sequence s;
     int64_t t0 = b, t1 = b + 1;
     if (a.q_start != nullptr) {
@@ -55,7 +63,7 @@ __device__ __forceinline__ Sequence sequence(const Fp4Attention &a, int32_t b, i
     s.news = static_cast<int32_t>(t1 - t0);
     s.length = static_cast<int32_t>(length);
     // rows of a call stay within 2^30
-    s.row_tiles = (s.news * group + tile_rows - 1) / tile_rows;
+    s.row_tiles = (s.news * d.group + d.tile_rows - 1) / d.tile_rows;
     return s;
 }
 
@@ -63,35 +71,33 @@ __device__ __forceinline__ Sequence sequence(const Fp4Attention &a, int32_t b, i
 struct Tile {
     int32_t row0, rows;
     int32_t first;      // the first token any row sees
-    int32_t begin;      // ... rounded down to 16 slots: where units count from
+    int32_t begin;      // ... rounded down to 32 slots: where units count from
     int32_t end;        // behind the last token any row sees; >= begin
     int32_t units;      // at least one
 };
 
-__device__ __forceinline__ Tile tile_of(const Sequence &s, int32_t rt, int32_t group,
-                                        int32_t tile_rows, int32_t window) {
+__device__ __forceinline__ Tile tile_of(const Sequence &s, const Division &d, int32_t rt) {
     Tile x;
-    x.row0 = rt * tile_rows;
-    x.rows = min(tile_rows, s.news * group - x.row0);
+    x.row0 = rt * d.tile_rows;
+    x.rows = min(d.tile_rows, s.news * d.group - x.row0);
     const int32_t ahead = s.length - s.news;   // query i sees tokens up to ahead + i
-    const int32_t q_lo = x.row0 / group, q_hi = (x.row0 + x.rows - 1) / group;
-    x.first = window > 0 ? max(0, ahead + q_lo + 1 - window) : 0;
-    x.begin = x.first & ~15;
+    const int32_t q_lo = x.row0 / d.group, q_hi = (x.row0 + x.rows - 1) / d.group;
+    x.first = d.window > 0 ? max(0, ahead + q_lo + 1 - d.window) : 0;
+    x.begin = x.first & ~31;
     x.end = max(x.begin, min(s.length, ahead + q_hi + 1));
-    x.units = max(1, (x.end - x.begin + kUnit - 1) / kUnit);
+    x.units = max(1, (x.end - x.begin + d.unit - 1) / d.unit);
     return x;
 }
 
-// Cost of all row tiles of one head, of a whole warp's sequences at once: few
+// Cost of all row tiles of one set of heads, of a whole warp's sequences at once: few
 // tiles are summed by the lane that has the sequence, many by all lanes.
-__device__ __forceinline__ int64_t head_cost(const Sequence &mine, int32_t group, int32_t tile_rows,
-                                             int32_t window) {
+__device__ __forceinline__ int64_t set_cost(const Sequence &mine, const Division &d) {
     constexpr int32_t kFew = 4;
     const int32_t lane = threadIdx.x % 32;
     int64_t cost = 0;
     if (mine.row_tiles <= kFew)
         for (int32_t rt = 0; rt < mine.row_tiles; ++rt)
-            cost += tile_of(mine, rt, group, tile_rows, window).units + kItemCost;
+            cost += tile_of(mine, d, rt).units + kItemCost;
     for (uint32_t many = __ballot_sync(0xFFFFFFFFu, mine.row_tiles > kFew); many; many &= many - 1) {
         const int32_t from = __ffs(many) - 1;
         Sequence s;
@@ -101,7 +107,7 @@ __device__ __forceinline__ int64_t head_cost(const Sequence &mine, int32_t group
         s.row_tiles = __shfl_sync(0xFFFFFFFFu, mine.row_tiles, from);
         int64_t sum = 0;
         for (int32_t rt = lane; rt < s.row_tiles; rt += 32)
-            sum += tile_of(s, rt, group, tile_rows, window).units + kItemCost;
+            sum += tile_of(s, d, rt).units + kItemCost;
 #pragma unroll
         for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
         if (lane == from) cost = sum;
@@ -127,8 +133,8 @@ struct Run {
 // Called by all kWarps warps of the block; holds two block barriers (one when
 // the run is empty).
 template <int kWarps>
-__device__ __forceinline__ Run block_run(const Fp4Attention &a, int32_t group, int32_t tile_rows,
-                                         uint32_t *error, PlanShared<kWarps> &sm) {
+__device__ __forceinline__ Run block_run(const Fp4Attention &a, const Division &d, uint32_t *error,
+                                         PlanShared<kWarps> &sm) {
     constexpr int32_t kThreads = 32 * kWarps;
     const int32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int32_t per_thread = (a.batch + kThreads - 1) / kThreads;
@@ -139,8 +145,8 @@ __device__ __forceinline__ Run block_run(const Fp4Attention &a, int32_t group, i
     int64_t mine = 0;
     for (int32_t i = 0; i < per_thread; ++i) {
         const Sequence s = b0 + i < a.batch
-            ? sequence(a, static_cast<int32_t>(b0 + i), group, tile_rows, &bad) : none;
-        mine += head_cost(s, group, tile_rows, a.window) * a.pools.heads;
+            ? sequence(a, d, static_cast<int32_t>(b0 + i), &bad) : none;
+        mine += set_cost(s, d) * d.sets;
     }
     if (bad) atomicOr(error, kFp4ErrSequence);
     int64_t incl = mine;
@@ -168,8 +174,8 @@ __device__ __forceinline__ Run block_run(const Fp4Attention &a, int32_t group, i
     if (__any_sync(0xFFFFFFFFu, here)) {
         for (int32_t i = 0; i < per_thread; ++i) {
             const Sequence s = b0 + i < a.batch
-                ? sequence(a, static_cast<int32_t>(b0 + i), group, tile_rows, &bad) : none;
-            const int64_t n = head_cost(s, group, tile_rows, a.window) * a.pools.heads;
+                ? sequence(a, d, static_cast<int32_t>(b0 + i), &bad) : none;
+            const int64_t n = set_cost(s, d) * d.sets;
             if (here && before <= r.at && r.at < before + n) {
                 sm.seq = static_cast<int32_t>(b0 + i);
                 sm.base = before;
@@ -186,25 +192,24 @@ __device__ __forceinline__ Run block_run(const Fp4Attention &a, int32_t group, i
 // Walks the items of a run, one warp; every lane holds the same state.
 struct Walk {
     Sequence s;
-    int32_t seq, head, rt;
+    int32_t seq, set, rt;
     int64_t start;      // of the item on the axis
 
-    __device__ __forceinline__ void begin(const Fp4Attention &a, const Run &r, int32_t group,
-                                          int32_t tile_rows) {
+    __device__ __forceinline__ void begin(const Fp4Attention &a, const Division &d, const Run &r) {
         const int32_t lane = threadIdx.x % 32;
         bool bad = false;
         seq = r.seq;
-        s = sequence(a, seq, group, tile_rows, &bad);
+        s = sequence(a, d, seq, &bad);
         Sequence own = s;
         if (lane != 0) own.row_tiles = 0;
-        const int64_t cost = __shfl_sync(0xFFFFFFFFu, head_cost(own, group, tile_rows, a.window), 0);
-        head = static_cast<int32_t>((r.at - r.base) / cost);
-        start = r.base + head * cost;
+        const int64_t cost = __shfl_sync(0xFFFFFFFFu, set_cost(own, d), 0);
+        set = static_cast<int32_t>((r.at - r.base) / cost);
+        start = r.base + set * cost;
         rt = 0;
         for (int32_t first = 0;; first += 32) {   // the tile that holds r.at
             int32_t n = 0;
             if (first + lane < s.row_tiles)
-                n = tile_of(s, first + lane, group, tile_rows, a.window).units + kItemCost;
+                n = tile_of(s, d, first + lane).units + kItemCost;
             int64_t incl = n;
 #pragma unroll
             for (int o = 1; o < 32; o *= 2) {
@@ -219,22 +224,21 @@ struct Walk {
                 return;
             }
             start += __shfl_sync(0xFFFFFFFFu, incl, 31);
-            if (first + 32 >= s.row_tiles) return;    // not reached: the run starts in this head
+            if (first + 32 >= s.row_tiles) return;    // not reached: the run starts in this set
         }
     }
 
     // To the next item; `cost` is the present one's.  False behind the last.
-    __device__ __forceinline__ bool next(const Fp4Attention &a, int64_t cost, int32_t group,
-                                         int32_t tile_rows) {
+    __device__ __forceinline__ bool next(const Fp4Attention &a, const Division &d, int64_t cost) {
         start += cost;
         if (++rt < s.row_tiles) return true;
         rt = 0;
-        if (++head < a.pools.heads) return true;
-        head = 0;
+        if (++set < d.sets) return true;
+        set = 0;
         bool bad = false;
         do {
             if (++seq >= a.batch) return false;
-            s = sequence(a, seq, group, tile_rows, &bad);
+            s = sequence(a, d, seq, &bad);
         } while (s.row_tiles == 0);
         return true;
     }
@@ -244,19 +248,19 @@ struct Walk {
 // behind it.
 struct Split {
     int32_t blocks;     // blocks that hold a part of the item; 0: no such item
-    int32_t token0, row0, rows, head;
+    int32_t token0, row0, rows, set;
 };
 
-// Workspace: Split [kMaxBlocks], then two parts for each block: rows x dim
-// sums, rows maxima and rows sums of weights.
+// Workspace: Split [kMaxBlocks], then two parts for each block: for each head
+// of the set rows x dim sums, rows maxima and rows sums of weights.
 __host__ __device__ constexpr int64_t part_floats(int rows, int dim) {
     return static_cast<int64_t>(rows) * (dim + 2);
 }
 constexpr int64_t kRecordBytes = (kMaxBlocks * sizeof(Split) + 15) / 16 * 16;
 
-__device__ __forceinline__ float *part_at(void *workspace, int64_t index, int rows, int dim) {
+__device__ __forceinline__ float *part_at(void *workspace, int64_t index, int64_t floats) {
     return reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kRecordBytes) +
-           index * part_floats(rows, dim);
+           index * floats;
 }
 
 }  // namespace fp4_plan
