@@ -176,7 +176,7 @@ struct Shape {
     static constexpr int kUnit = kStep * T;              // cached tokens of a round
     static constexpr int kBlocks = NT * D <= 128 ? 3 : 2;   // an SM holds: by registers
     static constexpr int kStages = D == 64 ? 5 : D == 256 ? 2 : NT == 1 ? 3 : 4;
-    static constexpr int kQPitch = 2 * D + 16;           // bytes: rows start in other banks
+    static constexpr int kQBytes = kRows * 2 * D;        // query rows of a head
     static constexpr int kHeadFloats = static_cast<int>(part_floats(kRows, D));
     static constexpr int64_t kPartFloats = static_cast<int64_t>(kHeads) * kHeadFloats;
 };
@@ -186,7 +186,7 @@ struct Shared {
     using S = Shape<D, NT, T>;
     alignas(128) uint8_t ring[S::kStages][4 * kWarps * S::kTile];
     // the query rows as they are, then in place as matrix operands
-    alignas(16) uint8_t q[2][S::kHeads][S::kRows][S::kQPitch];
+    alignas(16) uint8_t q[2][S::kHeads][S::kQBytes];
     // what the other warps of a head leave for the one that finishes it
     alignas(16) float4 sums[T > 1 ? kWarps : 1][T > 1 ? T - 1 : 1][T > 1 ? S::kOwn * NT : 1][T > 1 ? 32 : 1];
     alignas(8) uint64_t full[S::kStages];
@@ -212,15 +212,6 @@ __device__ __forceinline__ int32_t stage_at(bool by_tile, int32_t step, int32_t 
 
 // ---------------------------------------------------------------------------
 // the copying warp
-
-__device__ __forceinline__ void copy16_async(uint32_t dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
-}
-
-// Arrives at a barrier when this lane's copies so far have landed.
-__device__ __forceinline__ void copies_arrive(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(bar) : "memory");
-}
 
 template <int D, int NT, int T>
 __device__ __forceinline__ void copy_items(const Fp4Attention &a, Shared<D, NT, T> &sm, const Run &run,
@@ -248,7 +239,7 @@ __device__ __forceinline__ void copy_items(const Fp4Attention &a, Shared<D, NT, 
     const uint8_t *pool = m < 2 ? a.pools.k : a.pools.v;
 
     Walk walk;
-    walk.begin(a, d, run);
+    walk.begin(d, run);
     for (;;) {
         const Tile x = tile_of(walk.s, d, walk.rt);
         const int64_t unit0 = walk.start + kItemCost;
@@ -298,19 +289,25 @@ __device__ __forceinline__ void copy_items(const Fp4Attention &a, Shared<D, NT, 
                     record->row0 = it.row0;
                     record->rows = it.rows;
                     record->set = it.set;
-                    record->blocks = static_cast<int32_t>((unit0 + x.units - 1) / run.per_block) - blockIdx.x + 1;
+                    record->blocks = static_cast<int32_t>(quotient(unit0 + x.units - 1, run.per_block)) - blockIdx.x + 1;
                 }
             }
-            constexpr int kPieces = D / 8;     // of a row
-            for (int32_t i = lane; i < kHeads * x.rows * kPieces; i += 32) {
-                const int32_t r = i / kPieces, h = r / x.rows, row = x.row0 + r - h * x.rows;
-                const int32_t qi = walk.s.news > 1 ? row / d.group : 0;
-                const uint16_t *src = a.q + (it.token0 + qi) * a.q_stride +
-                    ((static_cast<int64_t>(it.set) * kHeads + h) * d.group + (row - qi * d.group)) * D;
-                copy16_async(smem_addr(sm.q[slot][h][row - x.row0]) + 16 * (i % kPieces), src + 8 * (i % kPieces));
-            }
-            copies_arrive(smem_addr(&sm.item_full[slot]));
-            if (lane == 0) barrier_arrive(smem_addr(&sm.item_full[slot]));
+            // The query rows, behind the first tiles: those take longer.  The
+            // rows of one token and head lie side by side.
+            auto copy_rows = [&]() {
+                const uint32_t bar = smem_addr(&sm.item_full[slot]);
+                if (lane == 0) barrier_expect(bar, kHeads * x.rows * 2 * D);
+                __syncwarp();
+                const int32_t q_lo = walk.s.news > 1 ? x.row0 / d.group : 0;
+                for (int32_t i = lane / kHeads;; i += 32 / kHeads) {
+                    const int32_t qi = q_lo + i, h = lane % kHeads;
+                    const int32_t lo = max(x.row0, qi * d.group), hi = min(x.row0 + x.rows, (qi + 1) * d.group);
+                    if (lo >= hi) break;
+                    const uint16_t *src = a.q + (it.token0 + qi) * a.q_stride +
+                        ((static_cast<int64_t>(it.set) * kHeads + h) * d.group + (lo - qi * d.group)) * D;
+                    copy_async(smem_addr(sm.q[slot][h]) + (lo - x.row0) * 2 * D, src, (hi - lo) * 2 * D, bar);
+                }
+            };
             ++items;
 
             int32_t at = it.begin;
@@ -338,15 +335,18 @@ __device__ __forceinline__ void copy_items(const Fp4Attention &a, Shared<D, NT, 
                 }
                 if (++stage == S::kStages) stage = 0, ++lap;
                 now = next;
+                if (r == 0) copy_rows();
             }
+            if (it.rounds == 0) copy_rows();
         }
         if (!walk.next(a, d, x.units + kItemCost)) break;
     }
     const uint32_t slot = items % 2;
     if (items >= 2) barrier_wait(smem_addr(&sm.item_empty[slot]), (items / 2 - 1) & 1, &sm.gave_up);
-    if (lane == 0) sm.item[slot].rounds = -1;
-    copies_arrive(smem_addr(&sm.item_full[slot]));
-    if (lane == 0) barrier_arrive(smem_addr(&sm.item_full[slot]));
+    if (lane == 0) {
+        sm.item[slot].rounds = -1;
+        barrier_arrive(smem_addr(&sm.item_full[slot]));
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -360,7 +360,7 @@ __device__ __forceinline__ void prepare_rows(const Fp4Attention &a, int32_t rows
                                              float (&c)[NT][2]) {
     using S = Shape<D, NT, T>;
     const int32_t share = threadIdx.x / 32 % T, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-    static_assert(NT * (D / 32) * 512 <= S::kRows * S::kQPitch, "the operands fit where the rows were");
+    static_assert(NT * (D / 32) * 512 == S::kQBytes, "the operands take the place of the rows");
     uint4 x[NT][D / 32];                   // dimensions [t D/4, (t + 1) D/4) of row g
     float scale[NT];
 #pragma unroll
@@ -370,7 +370,7 @@ __device__ __forceinline__ void prepare_rows(const Fp4Attention &a, int32_t rows
         for (int i = 0; i < D / 32; ++i) {
             x[n][i] = make_uint4(0, 0, 0, 0);
             if (live)
-                x[n][i] = *reinterpret_cast<const uint4 *>(q + (n * 8 + g) * S::kQPitch + t * (D / 2) + 16 * i);
+                x[n][i] = *reinterpret_cast<const uint4 *>(q + (n * 8 + g) * 2 * D + t * (D / 2) + 16 * i);
         }
         uint32_t most = 0;                 // largest magnitude pattern
 #pragma unroll
@@ -561,8 +561,8 @@ __device__ __forceinline__ void compute_items(const Fp4Attention &a, Shared<D, N
         if (it.rounds < 0) return;
 
         float c[NT][2];
-        prepare_rows<D, NT, T>(a, it.rows, sm.q[slot][hh][0], k_scale, c);
-        const uint4 *rows = reinterpret_cast<const uint4 *>(sm.q[slot][hh][0]);
+        prepare_rows<D, NT, T>(a, it.rows, sm.q[slot][hh], k_scale, c);
+        const uint4 *rows = reinterpret_cast<const uint4 *>(sm.q[slot][hh]);
         float top[NT][2], ref[NT][2], sum[NT][2];  // ref: what scores are taken against
         float o[S::kMTiles][NT][4];
 #pragma unroll
@@ -784,6 +784,8 @@ __device__ __forceinline__ void compute_items(const Fp4Attention &a, Shared<D, N
                 }
             }
         }
+        // the operands were plain writes, and copies take their place
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         if (T > 1) meet();                     // the sums may be written again
         else __syncwarp();
         if (lane == 0) barrier_arrive(smem_addr(&sm.item_empty[slot]));
@@ -809,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, T>::kBlocks)) fp4_atte
     }
     if (threadIdx.x == 0) sm.gave_up = 0;
     if (threadIdx.x < 2) {
-        barrier_init(smem_addr(&sm.item_full[threadIdx.x]), 33);   // the copying lanes, and the item itself
+        barrier_init(smem_addr(&sm.item_full[threadIdx.x]), 1);
         barrier_init(smem_addr(&sm.item_empty[threadIdx.x]), kWarps);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -820,11 +822,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, T>::kBlocks)) fp4_atte
     load_scales(a, &k_scale, &v_scale);
     Split *record = static_cast<Split *>(a.workspace) + blockIdx.x;
     if (threadIdx.x == 32 * kWarps) record->blocks = 0;
+    const Run run = block_run<kWarps + 1>(a, d, &g_fp4_attention_error, sm.plan);
     if (!fp4_scale_ok(k_scale) || !fp4_scale_ok(v_scale)) {
         if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_fp4_attention_error, kFp4ErrScale);
         return;
     }
-    const Run run = block_run<kWarps + 1>(a, d, &g_fp4_attention_error, sm.plan);
     if (run.at >= run.end) return;             // the whole block
     if (threadIdx.x >= 32 * kWarps)
         copy_items<D, NT, T>(a, sm, run, d, record);
@@ -860,16 +862,20 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 2) fp4_attention_join_kernel(
     const int32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     int32_t c = blockIdx.x;
     if (search > 0) {                              // in the records of so many blocks
-        if (threadIdx.x == 0) found = -1;
-        __syncthreads();
         if (warp == 0) {
-            int32_t before = 0;
-            for (int32_t first = 0; first < search && before <= c; first += 32) {
-                const bool split = first + lane < search && records[first + lane].blocks > 0;
-                const uint32_t those = __ballot_sync(0xFFFFFFFFu, split);
-                if (split && before + __popc(those & ((1u << lane) - 1)) == c) found = first + lane;
-                before += __popc(those);
+            int32_t mine = -1, before = 0;
+            uint32_t those[(kMaxBlocks + 31) / 32];
+#pragma unroll
+            for (int k = 0; k < (kMaxBlocks + 31) / 32; ++k)
+                those[k] = 32 * k + lane < search ? records[32 * k + lane].blocks : 0;
+#pragma unroll
+            for (int k = 0; k < (kMaxBlocks + 31) / 32; ++k) {
+                those[k] = __ballot_sync(0xFFFFFFFFu, those[k] != 0);
+                const int32_t n = __popc(those[k]);
+                if (c >= before && c < before + n) mine = 32 * k + __fns(those[k], 0, c - before + 1);
+                before += n;
             }
+            if (lane == 0) found = mine;
         }
         __syncthreads();
         if (found < 0) return;

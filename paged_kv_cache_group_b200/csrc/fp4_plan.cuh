@@ -67,6 +67,12 @@ __device__ __forceinline__ Sequence sequence(const Fp4Attention &a, const Divisi
     return s;
 }
 
+// a / b for a >= 0, b > 0: places on the axis hardly ever need 64 bits.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 // The rows of one tile of a sequence and the cached tokens they see.
 struct Tile {
     int32_t row0, rows;
@@ -81,7 +87,8 @@ __device__ __forceinline__ Tile tile_of(const Sequence &s, const Division &d, in
     x.row0 = rt * d.tile_rows;
     x.rows = min(d.tile_rows, s.news * d.group - x.row0);
     const int32_t ahead = s.length - s.news;   // query i sees tokens up to ahead + i
-    const int32_t q_lo = x.row0 / d.group, q_hi = (x.row0 + x.rows - 1) / d.group;
+    const int32_t q_lo = s.news > 1 ? x.row0 / d.group : 0;
+    const int32_t q_hi = s.news > 1 ? (x.row0 + x.rows - 1) / d.group : 0;
     x.first = d.window > 0 ? max(0, ahead + q_lo + 1 - d.window) : 0;
     x.begin = x.first & ~31;
     x.end = max(x.begin, min(s.length, ahead + q_hi + 1));
@@ -118,7 +125,8 @@ __device__ __forceinline__ int64_t set_cost(const Sequence &mine, const Division
 template <int kWarps>
 struct PlanShared {
     int64_t scan[kWarps];
-    int64_t base;
+    int64_t base, cost;
+    Sequence s;
     int32_t seq;
 };
 
@@ -127,6 +135,8 @@ struct Run {
     int64_t at, end;     // [at, end); empty: no work
     int64_t per_block;
     int64_t base;        // start of sequence `seq` on the axis
+    int64_t cost;        // of one of its sets of heads
+    Sequence s;
     int32_t seq;
 };
 
@@ -139,15 +149,16 @@ __device__ __forceinline__ Run block_run(const Fp4Attention &a, const Division &
     const int32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int32_t per_thread = (a.batch + kThreads - 1) / kThreads;
     const int64_t b0 = static_cast<int64_t>(threadIdx.x) * per_thread;
-    Sequence none;
-    none.token0 = none.news = none.length = none.row_tiles = 0;
     bool bad = false;
-    int64_t mine = 0;
-    for (int32_t i = 0; i < per_thread; ++i) {
-        const Sequence s = b0 + i < a.batch
-            ? sequence(a, d, static_cast<int32_t>(b0 + i), &bad) : none;
-        mine += set_cost(s, d) * d.sets;
-    }
+    auto look = [&](int32_t i) {
+        Sequence s;
+        s.token0 = s.news = s.length = s.row_tiles = 0;
+        if (b0 + i < a.batch) s = sequence(a, d, static_cast<int32_t>(b0 + i), &bad);
+        return s;
+    };
+    Sequence s = look(0);                      // most often the only one
+    int64_t cost = set_cost(s, d), mine = cost * d.sets;
+    for (int32_t i = 1; i < per_thread; ++i) mine += set_cost(look(i), d) * d.sets;
     if (bad) atomicOr(error, kFp4ErrSequence);
     int64_t incl = mine;
 #pragma unroll
@@ -164,28 +175,32 @@ __device__ __forceinline__ Run block_run(const Fp4Attention &a, const Division &
         total += sm.scan[w];
     }
     Run r;
-    r.per_block = (total + gridDim.x - 1) / gridDim.x;
+    r.per_block = quotient(total + gridDim.x - 1, gridDim.x);
     r.at = r.per_block * blockIdx.x;
     r.end = min(total, r.at + r.per_block);
     r.seq = 0;
-    r.base = 0;
+    r.base = r.cost = 0;
     if (r.at >= r.end) return r;
     const bool here = mine > 0 && before <= r.at && r.at < before + mine;
     if (__any_sync(0xFFFFFFFFu, here)) {
-        for (int32_t i = 0; i < per_thread; ++i) {
-            const Sequence s = b0 + i < a.batch
-                ? sequence(a, d, static_cast<int32_t>(b0 + i), &bad) : none;
-            const int64_t n = set_cost(s, d) * d.sets;
-            if (here && before <= r.at && r.at < before + n) {
+        for (int32_t i = 0;; ++i) {
+            if (here && before <= r.at && r.at < before + cost * d.sets) {
                 sm.seq = static_cast<int32_t>(b0 + i);
                 sm.base = before;
+                sm.cost = cost;
+                sm.s = s;
             }
-            before += n;
+            if (i + 1 >= per_thread) break;
+            before += cost * d.sets;
+            s = look(i + 1);
+            cost = set_cost(s, d);
         }
     }
     __syncthreads();
     r.seq = sm.seq;
     r.base = sm.base;
+    r.cost = sm.cost;
+    r.s = sm.s;
     return r;
 }
 
@@ -195,18 +210,14 @@ struct Walk {
     int32_t seq, set, rt;
     int64_t start;      // of the item on the axis
 
-    __device__ __forceinline__ void begin(const Fp4Attention &a, const Division &d, const Run &r) {
+    __device__ __forceinline__ void begin(const Division &d, const Run &r) {
         const int32_t lane = threadIdx.x % 32;
-        bool bad = false;
         seq = r.seq;
-        s = sequence(a, d, seq, &bad);
-        Sequence own = s;
-        if (lane != 0) own.row_tiles = 0;
-        const int64_t cost = __shfl_sync(0xFFFFFFFFu, set_cost(own, d), 0);
-        set = static_cast<int32_t>((r.at - r.base) / cost);
-        start = r.base + set * cost;
+        s = r.s;
+        set = static_cast<int32_t>(quotient(r.at - r.base, r.cost));
+        start = r.base + set * r.cost;
         rt = 0;
-        for (int32_t first = 0;; first += 32) {   // the tile that holds r.at
+        for (int32_t first = 0; s.row_tiles > 1; first += 32) {   // the tile that holds r.at
             int32_t n = 0;
             if (first + lane < s.row_tiles)
                 n = tile_of(s, d, first + lane).units + kItemCost;
