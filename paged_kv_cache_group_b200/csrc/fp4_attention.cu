@@ -838,116 +838,233 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, T>::kBlocks)) fp4_atte
 // ---------------------------------------------------------------------------
 // the join
 
-constexpr int kJoinWarps = 16;         // at most, of a block
-
-// Block (c, y) merges some dimensions of one head of the item that began in
-// block c, or with few items of the c-th item that is split: `units` of the
-// 32-lane, 4-value fragments its parts are stored in, a warp each, and where
-// it has more warps its parts are dealt out over them.  The parts are met once,
-// with a running maximum like the tokens were, four of them under way at a time:
-// more cost registers, and with them the blocks that run side by side.
-template <int D, int NT, int T>
-__global__ void __launch_bounds__(32 * kJoinWarps, 2) fp4_attention_join_kernel(const Fp4Attention a,
-                                                                             int32_t units,
-                                                                             int32_t search) {
-    using S = Shape<D, NT, T>;
-    constexpr int kRows = S::kRows;
-    constexpr int kBatch = 4;
-    __shared__ float4 share_x[kJoinWarps][32];
-    __shared__ float4 share_l[kJoinWarps][32];     // tops and sums of the two rows
-    __shared__ int32_t found;
-    pdl_wait();
-    pdl_allow_next();
-    const Split *records = static_cast<const Split *>(a.workspace);
-    const int32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    int32_t c = blockIdx.x;
-    if (search > 0) {                              // in the records of so many blocks
-        if (warp == 0) {
-            int32_t mine = -1, before = 0;
-            uint32_t those[(kMaxBlocks + 31) / 32];
-#pragma unroll
-            for (int k = 0; k < (kMaxBlocks + 31) / 32; ++k)
-                those[k] = 32 * k + lane < search ? records[32 * k + lane].blocks : 0;
-#pragma unroll
-            for (int k = 0; k < (kMaxBlocks + 31) / 32; ++k) {
-                those[k] = __ballot_sync(0xFFFFFFFFu, those[k] != 0);
-                const int32_t n = __popc(those[k]);
-                if (c >= before && c < before + n) mine = 32 * k + __fns(those[k], 0, c - before + 1);
-                before += n;
-            }
-            if (lane == 0) found = mine;
-        }
-        __syncthreads();
-        if (found < 0) return;
-        c = found;
-    }
-    const Split s = records[c];
-    if (s.blocks == 0) return;
-    float k_scale, v_scale;
-    load_scales(a, &k_scale, &v_scale);
-    const int32_t slices = S::kMTiles * NT / units;                // of a head
-    const int32_t hh = blockIdx.y / slices;
-    const int32_t groups = blockDim.x / 32 / units, which = warp / units;
-    const int32_t unit = (blockIdx.y % slices) * units + warp % units;   // i * NT + n
-    const int32_t col = (unit % NT) * 8 + 2 * (lane % 4);
-    float top[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    auto meet_one = [&](const float (&t)[2], const float (&n)[2], const float (&v)[4]) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float now = fmaxf(top[j], t[j]);
-            const float base = now == -INFINITY ? 0.0f : now;
-            const float f = exp2_fast(top[j] - base), e = exp2_fast(t[j] - base);
-            top[j] = now;
-            l[j] = l[j] * f + n[j] * e;
-            x[j] = x[j] * f + v[j] * e;
-            x[2 + j] = x[2 + j] * f + v[2 + j] * e;
-        }
-    };
-    for (int32_t i0 = which; i0 < s.blocks; i0 += groups * kBatch) {
-        float2 t[kBatch], n[kBatch];
-        float4 v[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const int32_t i = i0 + k * groups;
-            t[k] = make_float2(-INFINITY, -INFINITY), n[k] = make_float2(0.0f, 0.0f);
-            v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (i < s.blocks) {
-                // part 1 of block c, then part 0 of the blocks behind it
-                const float *p = part_at(a.workspace, 2 * static_cast<int64_t>(c + i) + (i == 0 ? 1 : 0),
-                                         S::kPartFloats) + hh * S::kHeadFloats;
-                t[k] = *reinterpret_cast<const float2 *>(p + kRows * D + col);
-                n[k] = *reinterpret_cast<const float2 *>(p + kRows * D + kRows + col);
-                v[k] = reinterpret_cast<const float4 *>(p)[unit * 32 + lane];
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-            meet_one({t[k].x, t[k].y}, {n[k].x, n[k].y}, {v[k].x, v[k].y, v[k].z, v[k].w});
-    }
-    if (groups > 1) {
-        if (which > 0) {
-            share_x[warp][lane] = make_float4(x[0], x[1], x[2], x[3]);
-            share_l[warp][lane] = make_float4(top[0], top[1], l[0], l[1]);
-        }
-        __syncthreads();
-        if (which > 0) return;
-        for (int32_t w = warp + units; w < groups * units; w += units) {
-            const float4 v = share_x[w][lane], m = share_l[w][lane];
-            meet_one({m.x, m.y}, {m.z, m.w}, {v.x, v.y, v.z, v.w});
-        }
-    }
-    const int32_t i = unit / NT;
+// Two columns of a fragment, divided by their sums and stored.
+template <int D>
+__device__ __forceinline__ void store_joined(const Fp4Attention &a, const Split &s, int32_t head, int32_t i,
+                                             int32_t col, const float (&x)[4], const float (&top)[2],
+                                             const float (&l)[2], float v_scale) {
+    const int32_t lane = threadIdx.x % 32;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int32_t row = col + j;
         if (row >= s.rows) continue;
-        const RowPlace p = row_place(s.token0, s.row0 + row, s.set * S::kHeads + hh, a.q_heads / a.pools.heads);
+        const RowPlace p = row_place(s.token0, s.row0 + row, head, a.q_heads / a.pools.heads);
         const float inv = row_factor(l[j], v_scale);
         *reinterpret_cast<uint32_t *>(a.out + p.token * a.out_stride + static_cast<int64_t>(p.q_head) * D +
                                       (lane / 4) * (D / 8) + 2 * i) = bf16x2_of(x[j] * inv, x[2 + j] * inv);
         if (a.lse != nullptr && i == 0 && lane < 4)
             a.lse[static_cast<int64_t>(p.token) * a.q_heads + p.q_head] = row_lse(top[j], l[j]);
     }
+}
+
+// Part i of the item that began in block c: part 1 of that block, then part 0
+// of the blocks behind it.
+template <int D, int NT, int T>
+__device__ __forceinline__ const float *joined_part(const Fp4Attention &a, int32_t c, int32_t i, int32_t hh) {
+    using S = Shape<D, NT, T>;
+    return part_at(a.workspace, 2 * static_cast<int64_t>(c + i) + (i == 0 ? 1 : 0), S::kPartFloats) +
+           hh * S::kHeadFloats;
+}
+
+constexpr int kJoinThreads = 256;
+constexpr int kJoinSlots = 12;
+constexpr int kJoinRefill = 4;          // slots filled again at once
+
+// Block (c, hh) merges head hh of the item that began in block c, its parts met
+// once with a running maximum like the tokens were.  An item has two or three
+// of them as a rule and dozens where one sequence is much longer than the rest;
+// fetching them costs one latency for twelve, without holding registers that
+// would keep other blocks away.
+template <int D, int NT, int T>
+__global__ void __launch_bounds__(kJoinThreads) fp4_attention_join_kernel(const Fp4Attention a) {
+    using S = Shape<D, NT, T>;
+    constexpr int kRows = S::kRows, kUnits = S::kMTiles * NT, kWarpsHere = kJoinThreads / 32;
+    constexpr int kMine = (kUnits + kWarpsHere - 1) / kWarpsHere;   // fragments of a warp
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    float (&slots)[kJoinSlots][S::kHeadFloats] = *reinterpret_cast<float (*)[kJoinSlots][S::kHeadFloats]>(smem_raw);
+    __shared__ alignas(8) uint64_t full[kJoinSlots];
+    __shared__ uint32_t gave_up;
+    const int32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x < kJoinSlots) barrier_init(smem_addr(&full[threadIdx.x]), 1);
+    if (threadIdx.x == 0) gave_up = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    __syncthreads();
+    pdl_wait();
+    pdl_allow_next();
+    const int32_t c = blockIdx.x, hh = blockIdx.y;
+    const Split s = static_cast<const Split *>(a.workspace)[c];
+    if (s.blocks == 0) return;
+    auto fetch = [&](int32_t i) {
+        const uint32_t bar = smem_addr(&full[i % kJoinSlots]);
+        barrier_expect(bar, S::kHeadFloats * 4);
+        copy_async(smem_addr(slots[i % kJoinSlots]), joined_part<D, NT, T>(a, c, i, hh), S::kHeadFloats * 4, bar);
+    };
+    if (threadIdx.x == 0)
+        for (int32_t i = 0; i < kJoinSlots && i < s.blocks; ++i) fetch(i);
+    float k_scale, v_scale;
+    load_scales(a, &k_scale, &v_scale);
+    float top[kMine][2], l[kMine][2], x[kMine][4];
+#pragma unroll
+    for (int m = 0; m < kMine; ++m) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) top[m][j] = -INFINITY, l[m][j] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[m][j] = 0.0f;
+    }
+    for (int32_t i = 0; i < s.blocks; ++i) {
+        barrier_wait(smem_addr(&full[i % kJoinSlots]), (i / kJoinSlots) & 1, &gave_up);
+        const float *p = slots[i % kJoinSlots];
+#pragma unroll
+        for (int m = 0; m < kMine; ++m) {
+            const int32_t unit = warp + m * kWarpsHere;    // i * NT + n
+            if (unit >= kUnits) continue;
+            const int32_t col = (unit % NT) * 8 + 2 * (lane % 4);
+            const float2 t = *reinterpret_cast<const float2 *>(p + kRows * D + col);
+            const float2 n = *reinterpret_cast<const float2 *>(p + kRows * D + kRows + col);
+            const float4 v = reinterpret_cast<const float4 *>(p)[unit * 32 + lane];
+            const float tt[2] = {t.x, t.y}, nn[2] = {n.x, n.y}, vv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float now = fmaxf(top[m][j], tt[j]);
+                const float base = now == -INFINITY ? 0.0f : now;
+                const float f = exp2_fast(top[m][j] - base), e = exp2_fast(tt[j] - base);
+                top[m][j] = now;
+                l[m][j] = l[m][j] * f + nn[j] * e;
+                x[m][j] = x[m][j] * f + vv[j] * e;
+                x[m][2 + j] = x[m][2 + j] * f + vv[2 + j] * e;
+            }
+        }
+        if (i % kJoinRefill == kJoinRefill - 1 && i + 1 + kJoinSlots - kJoinRefill < s.blocks) {
+            __syncthreads();                   // everybody has read the slots
+            if (threadIdx.x == 0)
+                for (int32_t k = i + 1 + kJoinSlots - kJoinRefill; k <= i + kJoinSlots && k < s.blocks; ++k) fetch(k);
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < kMine; ++m) {
+        const int32_t unit = warp + m * kWarpsHere;
+        if (unit < kUnits)
+            store_joined<D>(a, s, s.set * S::kHeads + hh, unit / NT, (unit % NT) * 8 + 2 * (lane % 4), x[m],
+                            top[m], l[m], v_scale);
+    }
+    if (*static_cast<volatile uint32_t *>(&gave_up)) __nanosleep(1000000);   // copies under way land
+}
+
+constexpr int kFewWarps = 16;
+
+// With few items each has many parts: block (c, y) merges fragment y of the
+// c-th item that is split, every warp some of the parts.  The maxima come first,
+// all at once, so that the sums wait for nothing but their own loads.
+template <int D, int NT, int T>
+__global__ void __launch_bounds__(32 * kFewWarps) fp4_attention_join_few_kernel(const Fp4Attention a,
+                                                                                int32_t blocks) {
+    using S = Shape<D, NT, T>;
+    constexpr int kRows = S::kRows, kUnits = S::kMTiles * NT;
+    constexpr int kTop = (kMaxBlocks * 8 + 32 * kFewWarps - 1) / (32 * kFewWarps);   // maxima a thread loads
+    constexpr int kBatch = 14;                 // sums under way
+    __shared__ float weight[kMaxBlocks][8];    // 2^(top of the part - top)
+    __shared__ float over_warps[kFewWarps][8];
+    __shared__ float4 share[kFewWarps][32];
+    __shared__ int32_t found;
+    pdl_wait();
+    pdl_allow_next();
+    const Split *records = static_cast<const Split *>(a.workspace);
+    const int32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (warp == 0) {
+        constexpr int kTurns = (kMaxBlocks + 31) / 32;
+        int32_t mine = -1, before = 0;
+        uint32_t those[kTurns];
+#pragma unroll
+        for (int k = 0; k < kTurns; ++k)
+            those[k] = 32 * k + lane < blocks ? records[32 * k + lane].blocks : 0;
+#pragma unroll
+        for (int k = 0; k < kTurns; ++k) {
+            those[k] = __ballot_sync(0xFFFFFFFFu, those[k] != 0);
+            const int32_t n = __popc(those[k]), c = blockIdx.x;
+            if (c >= before && c < before + n) mine = 32 * k + __fns(those[k], 0, c - before + 1);
+            before += n;
+        }
+        if (lane == 0) found = mine;
+    }
+    __syncthreads();
+    if (found < 0) return;
+    const int32_t c = found;
+    const Split s = records[c];
+    float k_scale, v_scale;
+    load_scales(a, &k_scale, &v_scale);
+    const int32_t hh = blockIdx.y / kUnits, unit = blockIdx.y % kUnits;   // unit: i * NT + n
+    const int32_t n8 = unit % NT * 8;          // its rows
+
+    // Thread: row threadIdx.x % 8 of every 64th part.
+    const int32_t row = n8 + threadIdx.x % 8;
+    float t[kTop], n[kTop];
+#pragma unroll
+    for (int k = 0; k < kTop; ++k) {
+        const int32_t i = threadIdx.x / 8 + k * (4 * kFewWarps);
+        t[k] = -INFINITY, n[k] = 0.0f;
+        if (i < s.blocks) {
+            const float *p = joined_part<D, NT, T>(a, c, i, hh);
+            t[k] = p[kRows * D + row];
+            n[k] = p[kRows * D + kRows + row];
+        }
+    }
+    auto over_rows = [&](float v, bool is_max) {
+        for (int o = 8; o < 32; o *= 2) {
+            const float w = __shfl_xor_sync(0xFFFFFFFFu, v, o);
+            v = is_max ? fmaxf(v, w) : v + w;
+        }
+        __syncthreads();
+        if (lane < 8) over_warps[warp][lane] = v;
+        __syncthreads();
+        v = over_warps[0][threadIdx.x % 8];
+        for (int w = 1; w < kFewWarps; ++w)
+            v = is_max ? fmaxf(v, over_warps[w][threadIdx.x % 8]) : v + over_warps[w][threadIdx.x % 8];
+        return v;
+    };
+    float most = -INFINITY, l = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kTop; ++k) most = fmaxf(most, t[k]);
+    most = over_rows(most, true);
+    const float base = most == -INFINITY ? 0.0f : most;
+#pragma unroll
+    for (int k = 0; k < kTop; ++k) {
+        const int32_t i = threadIdx.x / 8 + k * (4 * kFewWarps);
+        const float f = exp2_fast(t[k] - base);
+        if (i < s.blocks) weight[i][threadIdx.x % 8] = f;
+        l += f * n[k];
+    }
+    l = over_rows(l, false);
+
+    const int32_t col = 2 * (lane % 4);
+    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int32_t i0 = warp; i0 < s.blocks; i0 += kFewWarps * kBatch) {
+        float4 v[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int32_t i = i0 + k * kFewWarps;
+            v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (i < s.blocks) v[k] = reinterpret_cast<const float4 *>(joined_part<D, NT, T>(a, c, i, hh))[unit * 32 + lane];
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int32_t i = i0 + k * kFewWarps;
+            if (i < s.blocks) {
+                const float f0 = weight[i][col], f1 = weight[i][col + 1];
+                x[0] += f0 * v[k].x, x[1] += f1 * v[k].y, x[2] += f0 * v[k].z, x[3] += f1 * v[k].w;
+            }
+        }
+    }
+    share[warp][lane] = make_float4(x[0], x[1], x[2], x[3]);
+    __syncthreads();
+    if (warp != 0) return;
+    for (int w = 1; w < kFewWarps; ++w) {
+        const float4 v = share[w][lane];
+        x[0] += v.x, x[1] += v.y, x[2] += v.z, x[3] += v.w;
+    }
+    // lane j of the warp holds row j % 8
+    const float tops[2] = {__shfl_sync(0xFFFFFFFFu, most, col), __shfl_sync(0xFFFFFFFFu, most, col + 1)};
+    const float sums[2] = {__shfl_sync(0xFFFFFFFFu, l, col), __shfl_sync(0xFFFFFFFFu, l, col + 1)};
+    store_joined<D>(a, s, s.set * S::kHeads + hh, unit / NT, n8 + col, x, tops, sums, v_scale);
 }
 
 // ---------------------------------------------------------------------------
@@ -985,16 +1102,29 @@ cudaError_t launch_tiles(const Fp4Attention &a, cudaStream_t stream) {
     int64_t grid = static_cast<int64_t>(sms) * S::kBlocks;
     if (grid > kMaxBlocks / 3 * S::kBlocks) grid = kMaxBlocks / 3 * S::kBlocks;
     if (items < grid && items * longest < grid) grid = items * longest;
-    e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), kThreads, kSmem, stream, a);
+    // Started only when the GPU is free: blocks placed beside those of another
+    // kernel found SMs set up for less shared memory, and the last third of them
+    // ran behind the others (256 sequences of 3001-6000 tokens: 171 us, not 131).
+    kernel<<<static_cast<unsigned>(grid), kThreads, kSmem, stream>>>(a);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    // Few items have many parts each: one fragment to a block of 16 warps.
-    constexpr int32_t kUnits = S::kMTiles * NT;
-    const bool few = items * 8 <= sms && items < grid;
-    const int32_t units = few ? 1 : kUnits < 8 ? kUnits : 8;
-    return launch_pdl(fp4_attention_join_kernel<D, NT, T>,
-                      dim3(static_cast<unsigned>(few ? items : grid),
-                           static_cast<unsigned>(S::kHeads * kUnits / units)),
-                      32 * (few ? kJoinWarps : 8), 0, stream, a, units, few ? static_cast<int32_t>(grid) : 0);
+    g_launch_count.fetch_add(1, std::memory_order_relaxed);
+    if (items * 8 <= sms && items < grid) {    // few items, and with them many parts of each
+        fp4_attention_join_few_kernel<D, NT, T>
+            <<<dim3(static_cast<unsigned>(items), S::kHeads * S::kMTiles * NT), 32 * kFewWarps, 0, stream>>>(
+                a, static_cast<int32_t>(grid));
+        e = cudaGetLastError();
+        if (e == cudaSuccess) g_launch_count.fetch_add(1, std::memory_order_relaxed);
+        return e;
+    }
+    constexpr size_t kJoinSmem = kJoinSlots * S::kHeadFloats * 4;
+    if constexpr (kJoinSmem > 48 * 1024) {
+        e = cudaFuncSetAttribute(fp4_attention_join_kernel<D, NT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(kJoinSmem));
+        if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(fp4_attention_join_kernel<D, NT, T>, dim3(static_cast<unsigned>(grid), S::kHeads),
+                      kJoinThreads, kJoinSmem, stream, a);
 }
 
 template <int D, int NT>
