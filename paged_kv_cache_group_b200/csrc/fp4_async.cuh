@@ -1,0 +1,85 @@
+// What the attention kernels of the 4-bit cache share: barriers and copies in
+// shared memory, and the last step of a row.
+#pragma once
+
+#include <cmath>
+
+#include "fp4_device.cuh"
+
+namespace fp8q {
+
+constexpr int kWaitTries = 1 << 20;    // polls of a barrier before giving up
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+__device__ __forceinline__ void barrier_init(uint32_t bar, uint32_t arrivals) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(bar), "r"(arrivals) : "memory");
+}
+
+__device__ __forceinline__ void barrier_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
+                 :: "r"(bar), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ bool barrier_done(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, uint32_t bytes,
+                                           uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
+                 "[%0], [%1], %2, [%3];" :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void barrier_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
+}
+
+// Waits for a phase of a barrier.  Gives up after a bounded number of polls,
+// and once a block has done so, after a few: its output is not valid then.
+__device__ __forceinline__ void barrier_wait(uint32_t bar, uint32_t parity, volatile uint32_t *gave_up,
+                                             uint32_t *error) {
+    for (int32_t tries = 0; !barrier_done(bar, parity); ++tries)
+        if (tries > kWaitTries || (tries > 1000 && *gave_up)) {
+            *gave_up = 1;
+            atomicOr(error, kFp4ErrWait);
+            break;
+        }
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void load_scales(const Fp4Attention &a, float *ks, float *vs) {
+    *ks = a.pools.scale_dev ? a.pools.scale_dev[0] : a.pools.k_scale;
+    *vs = a.pools.scale_dev ? a.pools.scale_dev[1] : a.pools.v_scale;
+}
+
+// The fp32 output of a row from its joined sums: nothing seen gives 0, a NaN
+// among the scores stays one.
+__device__ __forceinline__ float row_factor(float l, float v_scale) { return l == 0.0f ? 0.0f : v_scale / l; }
+__device__ __forceinline__ float row_lse(float most, float l, float shift) {
+    return l == 0.0f ? -INFINITY : kLn2 * (most + (log2f(l) - shift));
+}
+
+// The place of a row of an item in `out` and `lse`.
+struct RowPlace {
+    int32_t token, q_head;
+};
+__device__ __forceinline__ RowPlace row_place(int32_t token0, int32_t row, int32_t head, int32_t group) {
+    const int32_t qi = row / group;
+    return {token0 + qi, head * group + (row - qi * group)};
+}
+
+}  // namespace fp8q

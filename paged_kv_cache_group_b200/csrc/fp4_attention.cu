@@ -44,7 +44,7 @@
 
 #include <cmath>
 
-#include "fp4_device.cuh"
+#include "fp4_async.cuh"
 #include "fp4_plan.cuh"
 
 namespace fp8q {
@@ -53,37 +53,7 @@ namespace {
 
 __device__ uint32_t g_fp4_attention_error;
 
-constexpr int kWaitTries = 1 << 20;    // polls of a barrier before giving up
 constexpr float kShift = 15.0f;        // p is held as p * 2^15
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
-
-__device__ __forceinline__ uint32_t smem_addr(const void *p) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-__device__ __forceinline__ void barrier_init(uint32_t bar, uint32_t arrivals) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(bar), "r"(arrivals) : "memory");
-}
-
-__device__ __forceinline__ void barrier_expect(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
-                 :: "r"(bar), "r"(bytes) : "memory");
-}
-
-__device__ __forceinline__ bool barrier_done(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    return ok != 0;
-}
-
-__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, uint32_t bytes,
-                                           uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
-                 "[%0], [%1], %2, [%3];" :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
-}
 
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                     uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -107,41 +77,15 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     return d;
 }
 
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 using namespace fp4_plan;
 
 constexpr int kWarps = 4;              // warps that compute
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kStep = 32;              // cached tokens of a warp's step
 
-__device__ __forceinline__ void barrier_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
-}
-
-// Waits for a phase of a barrier.  Gives up after a bounded number of polls,
-// and once a block has done so, after a few: its output is not valid then.
-__device__ __forceinline__ void barrier_wait(uint32_t bar, uint32_t parity, volatile uint32_t *gave_up) {
-    for (int32_t tries = 0; !barrier_done(bar, parity); ++tries)
-        if (tries > kWaitTries || (tries > 1000 && *gave_up)) {
-            *gave_up = 1;
-            atomicOr(&g_fp4_attention_error, kFp4ErrWait);
-            break;
-        }
-}
-
 // The four computing warps meet.
 __device__ __forceinline__ void meet() {
     asm volatile("bar.sync 1, %0;" :: "n"(32 * kWarps) : "memory");
-}
-
-__device__ __forceinline__ void load_scales(const Fp4Attention &a, float *ks, float *vs) {
-    *ks = a.pools.scale_dev ? a.pools.scale_dev[0] : a.pools.k_scale;
-    *vs = a.pools.scale_dev ? a.pools.scale_dev[1] : a.pools.v_scale;
 }
 
 __device__ __forceinline__ uint32_t low_twice(uint32_t w) {
@@ -281,7 +225,7 @@ __device__ __forceinline__ void copy_items(const Fp4Attention &a, Shared<D, NT, 
             Place now = look_up(it.begin);
 
             const uint32_t slot = items % 2;
-            if (items >= 2) barrier_wait(smem_addr(&sm.item_empty[slot]), (items / 2 - 1) & 1, &sm.gave_up);
+            if (items >= 2) barrier_wait(smem_addr(&sm.item_empty[slot]), (items / 2 - 1) & 1, &sm.gave_up, &g_fp4_attention_error);
             if (lane == 0) {
                 sm.item[slot] = it;
                 if (it.part == 1) {
@@ -314,7 +258,7 @@ __device__ __forceinline__ void copy_items(const Fp4Attention &a, Shared<D, NT, 
             for (int32_t r = 0; r < it.rounds; ++r, at += S::kUnit) {
                 const Place next = look_up(at + S::kUnit);
                 const uint32_t full = smem_addr(&sm.full[stage]);
-                if (lap > 0) barrier_wait(smem_addr(&sm.empty[stage]), (lap - 1) & 1, &sm.gave_up);
+                if (lap > 0) barrier_wait(smem_addr(&sm.empty[stage]), (lap - 1) & 1, &sm.gave_up, &g_fp4_attention_error);
                 if (lane == 0) {
                     const int32_t lo = max(at, it.first & ~15), hi = min(it.end, at + S::kUnit);
                     barrier_expect(full, (hi > lo ? (hi - lo + 15) / 16 : 0) * 2 * kHeads * S::kTile);
@@ -342,7 +286,7 @@ __device__ __forceinline__ void copy_items(const Fp4Attention &a, Shared<D, NT, 
         if (!walk.next(a, d, x.units + kItemCost)) break;
     }
     const uint32_t slot = items % 2;
-    if (items >= 2) barrier_wait(smem_addr(&sm.item_empty[slot]), (items / 2 - 1) & 1, &sm.gave_up);
+    if (items >= 2) barrier_wait(smem_addr(&sm.item_empty[slot]), (items / 2 - 1) & 1, &sm.gave_up, &g_fp4_attention_error);
     if (lane == 0) {
         sm.item[slot].rounds = -1;
         barrier_arrive(smem_addr(&sm.item_full[slot]));
@@ -525,22 +469,6 @@ __device__ __forceinline__ void add_tile(const uint8_t *vt, int32_t lo, int32_t 
     }
 }
 
-// The fp32 output of a row from its joined sums: nothing seen gives 0, a NaN
-// among the scores stays one.
-__device__ __forceinline__ float row_factor(float l, float v_scale) { return l == 0.0f ? 0.0f : v_scale / l; }
-__device__ __forceinline__ float row_lse(float most, float l) {
-    return l == 0.0f ? -INFINITY : kLn2 * (most + (log2f(l) - kShift));
-}
-
-// The place of a row of an item in `out` and `lse`.
-struct RowPlace {
-    int32_t token, q_head;
-};
-__device__ __forceinline__ RowPlace row_place(int32_t token0, int32_t row, int32_t head, int32_t group) {
-    const int32_t qi = row / group;
-    return {token0 + qi, head * group + (row - qi * group)};
-}
-
 template <int D, int NT, int T>
 __device__ __forceinline__ void compute_items(const Fp4Attention &a, Shared<D, NT, T> &sm, const Division &d,
                                               float k_scale, float v_scale) {
@@ -556,7 +484,7 @@ __device__ __forceinline__ void compute_items(const Fp4Attention &a, Shared<D, N
     uint32_t stage = 0, phase = 0;
     for (uint32_t items = 0;; ++items) {
         const uint32_t slot = items % 2;
-        barrier_wait(smem_addr(&sm.item_full[slot]), (items / 2) & 1, &sm.gave_up);
+        barrier_wait(smem_addr(&sm.item_full[slot]), (items / 2) & 1, &sm.gave_up, &g_fp4_attention_error);
         const Item &it = sm.item[slot];
         if (it.rounds < 0) return;
 
@@ -582,7 +510,7 @@ __device__ __forceinline__ void compute_items(const Fp4Attention &a, Shared<D, N
         const int32_t rounds = it.rounds;
 
         for (int32_t r = 0; r < rounds; ++r, at += S::kUnit) {
-            barrier_wait(smem_addr(&sm.full[stage]), phase, &sm.gave_up);
+            barrier_wait(smem_addr(&sm.full[stage]), phase, &sm.gave_up, &g_fp4_attention_error);
             const uint8_t *ring = sm.ring[stage];
             const bool edge = at + kStep > all_hi || at < all_lo;
             if (T == 1 || at < it.end) {
@@ -780,7 +708,7 @@ __device__ __forceinline__ void compute_items(const Fp4Attention &a, Shared<D, N
                         for (int i = 0; i < S::kOwn; ++i) *reinterpret_cast<uint32_t *>(out + 2 * i) = packed[j][i];
                     }
                     if (a.lse != nullptr && step == 0 && g == 0)
-                        a.lse[static_cast<int64_t>(p.token) * a.q_heads + p.q_head] = row_lse(most[j], l[j]);
+                        a.lse[static_cast<int64_t>(p.token) * a.q_heads + p.q_head] = row_lse(most[j], l[j], kShift);
                 }
             }
         }
@@ -795,7 +723,7 @@ __device__ __forceinline__ void compute_items(const Fp4Attention &a, Shared<D, N
 template <int D, int NT, int T>
 __device__ __forceinline__ Division division(const Fp4Attention &a) {
     using S = Shape<D, NT, T>;
-    return {a.q_heads / a.pools.heads, S::kRows, a.pools.heads / S::kHeads, S::kUnit, a.window};
+    return {a.q_heads / a.pools.heads, S::kRows, a.pools.heads / S::kHeads, S::kUnit, a.window, 0};
 }
 
 template <int D, int NT, int T>
@@ -853,7 +781,7 @@ __device__ __forceinline__ void store_joined(const Fp4Attention &a, const Split 
         *reinterpret_cast<uint32_t *>(a.out + p.token * a.out_stride + static_cast<int64_t>(p.q_head) * D +
                                       (lane / 4) * (D / 8) + 2 * i) = bf16x2_of(x[j] * inv, x[2 + j] * inv);
         if (a.lse != nullptr && i == 0 && lane < 4)
-            a.lse[static_cast<int64_t>(p.token) * a.q_heads + p.q_head] = row_lse(top[j], l[j]);
+            a.lse[static_cast<int64_t>(p.token) * a.q_heads + p.q_head] = row_lse(top[j], l[j], kShift);
     }
 }
 
@@ -912,7 +840,7 @@ __global__ void __launch_bounds__(kJoinThreads) fp4_attention_join_kernel(const 
         for (int j = 0; j < 4; ++j) x[m][j] = 0.0f;
     }
     for (int32_t i = 0; i < s.blocks; ++i) {
-        barrier_wait(smem_addr(&full[i % kJoinSlots]), (i / kJoinSlots) & 1, &gave_up);
+        barrier_wait(smem_addr(&full[i % kJoinSlots]), (i / kJoinSlots) & 1, &gave_up, &g_fp4_attention_error);
         const float *p = slots[i % kJoinSlots];
 #pragma unroll
         for (int m = 0; m < kMine; ++m) {
@@ -1136,15 +1064,23 @@ cudaError_t launch_heads(const Fp4Attention &a, cudaStream_t stream) {
 
 }  // namespace
 
+// More than 16 rows a sequence on average: their tiles are shared.
+bool fp4_attention_by_rows(int64_t batch, int64_t num_tokens, int32_t group) {
+    return num_tokens * group > 16 * batch;
+}
+
 int64_t fp4_attention_workspace(int64_t batch, int64_t num_tokens, int32_t q_heads,
                                 int32_t kv_heads, int32_t dim) {
     if (batch == 0) return 0;
+    if (fp4_attention_by_rows(batch, num_tokens, q_heads / kv_heads)) return fp4_attention_rows_workspace(dim);
     const int rows = 8 * tiles_of(batch, num_tokens, q_heads / kv_heads, dim);
     const int64_t blocks = rows * dim <= 1024 ? kMaxBlocks : kMaxBlocks / 3 * 2;   // as Shape::kBlocks
     return kRecordBytes + blocks * 2 * 4 * (kWarps / warps_of_head(kv_heads)) * part_floats(rows, dim);
 }
 
 cudaError_t launch_fp4_attention(const Fp4Attention &a, cudaStream_t stream) {
+    if (fp4_attention_by_rows(a.batch, a.num_tokens, a.q_heads / a.pools.heads))
+        return launch_fp4_attention_rows(a, stream);
     const int nt = tiles_of(a.batch, a.num_tokens, a.q_heads / a.pools.heads, a.pools.dim);
     switch (a.pools.dim) {
     case 64: return nt == 1 ? launch_heads<64, 1>(a, stream) : launch_heads<64, 2>(a, stream);

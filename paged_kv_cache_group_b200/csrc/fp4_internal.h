@@ -67,6 +67,11 @@ int64_t fp4_attention_workspace(int64_t batch, int64_t num_tokens, int32_t q_hea
                                 int32_t kv_heads, int32_t dim);
 cudaError_t launch_fp4_attention(const Fp4Attention &a, cudaStream_t stream);
 
+// Its kernel for many rows to a KV head (fp4_attention_rows.cu).
+bool fp4_attention_by_rows(int64_t batch, int64_t num_tokens, int32_t group);
+int64_t fp4_attention_rows_workspace(int32_t dim);
+cudaError_t launch_fp4_attention_rows(const Fp4Attention &a, cudaStream_t stream);
+
 struct QkNormRope {
     const uint16_t *q = nullptr;
     const uint16_t *k = nullptr;
@@ -96,5 +101,6 @@ cudaError_t launch_qk_norm_rope(const QkNormRope &r, cudaStream_t stream);
 // the current device; the device must be idle.
 cudaError_t read_fp4_kv_error(uint32_t *bits, bool clear);
 cudaError_t read_fp4_attention_error(uint32_t *bits, bool clear);
+cudaError_t read_fp4_rows_error(uint32_t *bits, bool clear);
 
 }  // namespace fp8q

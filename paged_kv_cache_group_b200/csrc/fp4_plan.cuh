@@ -28,6 +28,7 @@ struct Division {
     int32_t sets;        // sets of KV heads
     int32_t unit;        // cached tokens of a unit
     int32_t window;
+    int32_t whole;       // items are not split: 0 or 1
 };
 
 // One sequence as the kernels see it: bad lengths and ranges are cut to what

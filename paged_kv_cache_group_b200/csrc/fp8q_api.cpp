@@ -518,11 +518,12 @@ FP8Q_API int32_t fp8_kv_graphs_ready(const int8_t *states, int64_t n) {
 
 FP8Q_API fp8q_status fp8q_device_error(uint32_t *bits_out, int32_t clear) {
     if (bits_out == nullptr) return FP8Q_EINVAL;
-    uint32_t bits[3] = {0, 0, 0};
+    uint32_t bits[4] = {0, 0, 0, 0};
     cudaError_t e = fp8q::read_device_error(&bits[0], clear != 0);   // waits for the device
     if (e == cudaSuccess) e = fp8q::read_fp4_kv_error(&bits[1], clear != 0);
     if (e == cudaSuccess) e = fp8q::read_fp4_attention_error(&bits[2], clear != 0);
-    *bits_out = bits[0] | bits[1] | bits[2];
+    if (e == cudaSuccess) e = fp8q::read_fp4_rows_error(&bits[3], clear != 0);
+    *bits_out = bits[0] | bits[1] | bits[2] | bits[3];
     return from_cuda(e);
 }
 
