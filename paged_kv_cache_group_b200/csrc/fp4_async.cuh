@@ -8,7 +8,8 @@
 
 namespace fp8q {
 
-constexpr int kWaitTries = 1 << 20;    // polls of a barrier before giving up
+constexpr int32_t kWaitTries = 200000;  // polls of a barrier before giving up
+constexpr uint32_t kSleepNs = 20000;    // of one poll, at most
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -25,11 +26,14 @@ __device__ __forceinline__ void barrier_expect(uint32_t bar, uint32_t bytes) {
                  :: "r"(bar), "r"(bytes) : "memory");
 }
 
+// Sleeps until the phase ends or a while has passed; a warp that polls takes
+// issue slots from those that compute.
 __device__ __forceinline__ bool barrier_done(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(bar), "r"(parity), "r"(kSleepNs) : "memory");
     return ok != 0;
 }
 
@@ -44,11 +48,11 @@ __device__ __forceinline__ void barrier_arrive(uint32_t bar) {
 }
 
 // Waits for a phase of a barrier.  Gives up after a bounded number of polls,
-// and once a block has done so, after a few: its output is not valid then.
+// and once a block has done so, at once: its output is not valid then.
 __device__ __forceinline__ void barrier_wait(uint32_t bar, uint32_t parity, volatile uint32_t *gave_up,
                                              uint32_t *error) {
-    for (int32_t tries = 0; !barrier_done(bar, parity); ++tries)
-        if (tries > kWaitTries || (tries > 1000 && *gave_up)) {
+    for (int32_t left = kWaitTries; !barrier_done(bar, parity); --left)
+        if (left == 0 || *gave_up) {
             *gave_up = 1;
             atomicOr(error, kFp4ErrWait);
             break;

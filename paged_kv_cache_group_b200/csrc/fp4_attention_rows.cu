@@ -7,15 +7,18 @@
 // tcgen05.mma, S = Q K^T (both operands K-major) and O += P V (P from tensor
 // memory, V with its dimensions as the contiguous axis), sums in tensor memory.
 //
-// Warps of a block: four that own a query row a thread (query rows to fp16,
-// softmax, output), four that own a cached token a thread (pages, codes to
-// fp16), and four of which one thread issues the products and one warp walks
-// the block's items.  Nothing is double-buffered: K of the next tile is expanded
-// while this one's softmax runs, V after this one's second product, and two
-// blocks of an SM fill each other's gaps (one with 256 dimensions).
+// Warps of a block: eight on the query rows, two threads a row and 64 of a
+// tile's columns each (query rows to fp16, softmax, output), four that own a
+// cached token a thread (pages, codes to fp16), one that issues the products
+// and one that walks the block's items.  Nothing is
+// double-buffered: K of the next tile is expanded while this one's softmax
+// runs, V after this one's second product, and two blocks of an SM fill each
+// other's gaps (one with 256 dimensions).  The next scores are formed before
+// this tile's weights are used, where tensor memory holds both.
 //
-// Bound by the exponentials: 16 a cycle and SM, 1024 cycles for a tile, where
-// the two products take 256 for each 64 dimensions.
+// Bound by the latency of a tile's chain (scores, softmax, weights, product)
+// and the exponentials in it: a warp alone takes 8 cycles for each, four of a
+// scheduler 4.6, which is why a row has two threads.
 //
 // Operands are exact as there: code * block scale in fp16, and a query row
 // scaled by a power of two.  The scores are taken against a reference that
@@ -37,7 +40,9 @@ __device__ uint32_t g_fp4_rows_error;
 
 constexpr int kRows = 128;             // query rows of a tile
 constexpr int kTokens = 128;           // cached tokens of a tile, a unit of the plan
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;       // eight warps on rows, four on tokens, four others
+constexpr int kTokenThread = 256;   // the first that owns a cached token
+constexpr int kIssueThread = 384;   // the first of the warp that issues the products
 constexpr float kShift = 11.0f;        // a weight is held as p * 2^11
 constexpr float kSlack = 4.0f;         // growth of the maximum that is let pass
 
@@ -53,7 +58,7 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[16]) {
         : "r"(addr) : "memory");
 }
 
-__device__ __forceinline__ void tmem_store16(uint32_t addr, const float (&v)[16]) {
+__device__ __forceinline__ void tmem_store(uint32_t addr, const float (&v)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
         "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
@@ -128,10 +133,12 @@ struct Layout {
     static constexpr int kBlocks = D == 256 ? 1 : 2;         // an SM holds
     static constexpr int kOperand = 128 * D * 2;             // bytes of Q, of K, of V
     // Columns of tensor memory: scores, sums, weights (two to a column), the
-    // weights in place of the scores where all three do not fit half of it.
+    // weights in place of the scores where all three do not fit half of it;
+    // then each half of a row replaces its own scores.
     static constexpr bool kApart = D != 128;
     static constexpr int kSumsAt = 128;
     static constexpr int kWeightsAt = kApart ? 128 + D : 0;
+    static constexpr int kWeightsHalf = kApart ? 32 : 64;    // columns from one half's weights to the other's
     static constexpr int kColumns = D == 256 ? 512 : 256;
     static constexpr int64_t kPartFloats = part_floats(kRows, D);
 };
@@ -140,6 +147,7 @@ struct Control {
     uint64_t item_full[2], item_empty[2];
     uint64_t q_full, k_full, v_full;     // operands are in shared memory
     uint64_t scores, weights, summed;    // S is there; P is there; P V is done
+    float halves[2][kRows];              // what the two threads of a row tell each other
     Item item[2];
     uint32_t gave_up, tmem;
     PlanShared<kThreads / 32> plan;
@@ -233,68 +241,74 @@ __device__ __forceinline__ void walk_items(const Fp4Attention &a, Control &c, co
 template <int D>
 __device__ __forceinline__ void expand_items(const Fp4Attention &a, Shared<D> &sm, const Waits &wait) {
     constexpr int kBlocks16 = D / 16;          // blocks of 16 dimensions
-    const int32_t row = threadIdx.x % 128;
+    const int32_t row = threadIdx.x - kTokenThread;
+    const uint32_t at_row = row * 128 + (row & 7) * 16;     // piece c: this ^ 16 c, in its panel
     const int32_t tiles = a.pools.tiles;
     const int32_t shift = (tiles & (tiles - 1)) == 0 ? __ffs(tiles) - 1 : -1;
     uint32_t n = 0;                            // tiles so far
     for (uint32_t items = 0;; ++items) {
         wait(sm.c.item_full[items % 2], items / 2);
-        const Item it = sm.c.item[items % 2];
+        const Item &shared = sm.c.item[items % 2];
+        const int32_t count = shared.tiles, begin = shared.begin, first = shared.first, end = shared.end;
+        const int32_t *table = a.block_table + static_cast<int64_t>(shared.seq) * a.table_stride;
+        const int64_t head = static_cast<int64_t>(shared.head) * tiles;
         warp_arrive(sm.c.item_empty[items % 2]);
-        if (it.tiles < 0) return;
-        const int32_t *table = a.block_table + static_cast<int64_t>(it.seq) * a.table_stride;
-        for (int32_t j = 0; j < it.tiles; ++j, ++n) {
-            const int32_t tok = it.begin + j * kTokens + row;
-            const bool live = tok >= it.first && tok < it.end;   // others count as zeros
+        if (count < 0) return;
+        for (int32_t j = 0; j < count; ++j, ++n) {
+            // Tokens no row sees count as zeros: a seen one's codes, no scale.
+            const int32_t mine = begin + j * kTokens + row;
+            const int32_t tok = max(first, min(mine, end - 1));
+            const int32_t at16 = tok / 16, slot = tok % 16;
+            const int32_t page_at = shift >= 0 ? at16 >> shift : at16 / tiles;
+            int64_t page = table[page_at];
+            if (page < 0 || page >= a.pools.num_blocks) {
+                atomicOr(&g_fp4_rows_error, kFp4ErrSlot);
+                page = 0;
+            }
+            const int64_t tile = page * a.pools.block_stride + (head + (at16 - page_at * tiles)) * (9 * D);
+            const uint8_t *kt = a.pools.k + tile, *vt = a.pools.v + tile;
             uint2 kc[kBlocks16], vc[kBlocks16];
-            uint32_t kz[(kBlocks16 + 3) / 4], vz[kBlocks16];
+            uint32_t kz[kBlocks16 / 4], vz[kBlocks16];
 #pragma unroll
-            for (int b = 0; b < kBlocks16; ++b) kc[b] = vc[b] = make_uint2(0, 0), vz[b] = 0;
+            for (int b = 0; b < kBlocks16; b += 2) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(kt + slot * (D / 2) + 8 * b);
+                kc[b] = make_uint2(x.x, x.y), kc[b + 1] = make_uint2(x.z, x.w);
+            }
 #pragma unroll
-            for (int b = 0; b < kBlocks16 / 4; ++b) kz[b] = 0;
-            if (live) {
-                const int32_t at16 = tok / 16, slot = tok % 16;
-                const int32_t page_at = shift >= 0 ? at16 >> shift : at16 / tiles;
-                int64_t page = table[page_at];
-                if (page < 0 || page >= a.pools.num_blocks) {
-                    atomicOr(&g_fp4_rows_error, kFp4ErrSlot);
-                    page = 0;
-                }
-                const int64_t tile = page * a.pools.block_stride +
-                    (static_cast<int64_t>(it.head) * tiles + (at16 - page_at * tiles)) * (9 * D);
-                const uint8_t *kt = a.pools.k + tile, *vt = a.pools.v + tile;
-#pragma unroll
-                for (int b = 0; b < kBlocks16; b += 2) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(kt + slot * (D / 2) + 8 * b);
-                    kc[b] = make_uint2(x.x, x.y), kc[b + 1] = make_uint2(x.z, x.w);
-                }
-#pragma unroll
-                for (int b = 0; b < kBlocks16 / 4; ++b)
-                    kz[b] = *reinterpret_cast<const uint32_t *>(kt + 8 * D + slot * kBlocks16 + 4 * b);
+            for (int b = 0; b < kBlocks16 / 4; ++b) {
+                kz[b] = *reinterpret_cast<const uint32_t *>(kt + 8 * D + slot * kBlocks16 + 4 * b);
+                if (mine != tok) kz[b] = 0;
+            }
+            auto load_v = [&]() {
 #pragma unroll
                 for (int b = 0; b < kBlocks16; ++b) {
                     vc[b] = *reinterpret_cast<const uint2 *>(vt + b * 128 + slot * 8);
                     vz[b] = vt[8 * D + b * 16 + slot];
+                    if (mine != tok) vz[b] = 0;
                 }
-            }
-            auto write = [&](uint8_t *dst, int32_t b, uint2 codes, uint32_t scale) {
-                const uint32_t s = f16x2_of_e4m3x2(scale * 0x101u);
+            };
+            if (D != 128) load_v();            // at once where there are registers for both
+            // `scale`: a block's scale byte twice
+            auto write = [&](uint8_t *dst, int b, uint2 codes, uint32_t scale) {
+                const uint32_t s = f16x2_of_e4m3x2(scale);
                 uint32_t x[4];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     f16x2_of_e2m1x8(h ? codes.y : codes.x, x);
-                    *reinterpret_cast<uint4 *>(dst + piece_at(row, 2 * b + h)) =
+                    const int c = 2 * b + h;
+                    *reinterpret_cast<uint4 *>(dst + c / 8 * (128 * 128) + (at_row ^ (c % 8 * 16))) =
                         make_uint4(mul_f16x2(x[0], s), mul_f16x2(x[1], s), mul_f16x2(x[2], s), mul_f16x2(x[3], s));
                 }
             };
             if (n > 0) wait(sm.c.scores, n - 1);       // the last product with K is done
 #pragma unroll
-            for (int b = 0; b < kBlocks16; ++b) write(sm.k, b, kc[b], (kz[b / 4] >> (8 * (b % 4))) & 0xFFu);
+            for (int b = 0; b < kBlocks16; ++b) write(sm.k, b, kc[b], __byte_perm(kz[b / 4], 0, 0x11 * (b % 4)));
             operands_written();
             warp_arrive(sm.c.k_full);
+            if (D == 128) load_v();
             if (n > 0) wait(sm.c.summed, n - 1);       // ... and with V
 #pragma unroll
-            for (int b = 0; b < kBlocks16; ++b) write(sm.v, b, vc[b], vz[b]);
+            for (int b = 0; b < kBlocks16; ++b) write(sm.v, b, vc[b], vz[b] * 0x101u);
             operands_written();
             warp_arrive(sm.c.v_full);
         }
@@ -302,43 +316,71 @@ __device__ __forceinline__ void expand_items(const Fp4Attention &a, Shared<D> &s
 }
 
 // ---------------------------------------------------------------------------
-// the thread that issues the products
+// the warp that issues the products
 
+// True for one lane of a converged warp.
+__device__ __forceinline__ bool one_lane() {
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes != 0;
+}
+
+// All lanes run the same loops, so that operands are in uniform registers when
+// one of them issues: a single thread's took 100 to 200 cycles a product.
 template <int D>
 __device__ __forceinline__ void issue_items(Shared<D> &sm, const Waits &wait, uint32_t tmem) {
     using L = Layout<D>;
-    const uint32_t q = smem_addr(sm.q), k = smem_addr(sm.k), v = smem_addr(sm.v);
+    const uint64_t q = operand(smem_addr(sm.q), 16), k = operand(smem_addr(sm.k), 16),
+                   v = operand(smem_addr(sm.v), 128 * 128);
     uint32_t n = 0, full = 0;                  // tiles, and items with any
     for (uint32_t items = 0;; ++items) {
         wait(sm.c.item_full[items % 2], items / 2);
-        const int32_t tiles = sm.c.item[items % 2].tiles;
-        barrier_arrive(smem_addr(&sm.c.item_empty[items % 2]));
+        const int32_t tiles = __shfl_sync(0xFFFFFFFFu, sm.c.item[items % 2].tiles, 0);
+        warp_arrive(sm.c.item_empty[items % 2]);
         if (tiles < 0) return;
-        if (tiles > 0) wait(sm.c.q_full, full++);
-        for (int32_t j = 0; j < tiles; ++j, ++n) {
-            wait(sm.c.k_full, n);
-            if (!L::kApart && n > 0) wait(sm.c.summed, n - 1);   // the weights lie where the scores go
+        if (tiles == 0) continue;
+        wait(sm.c.q_full, full++);
+        auto scores = [&](uint32_t at) {       // S of a tile
+            wait(sm.c.k_full, at);
+            __syncwarp();
             tmem_after();
+            if (one_lane()) {
 #pragma unroll
-            for (int s = 0; s < D / 16; ++s) {
-                const uint32_t at = (s / 4) * (128 * 128) + (s % 4) * 32;
-                mma_shared(tmem, operand(q + at, 16), operand(k + at, 16), instruction(kTokens, false), s > 0);
+                for (int s = 0; s < D / 16; ++s) {
+                    const int off = ((s / 4) * (128 * 128) + (s % 4) * 32) >> 4;
+                    mma_shared(tmem, q + off, k + off, instruction(kTokens, false), s > 0);
+                }
+                mma_arrive(smem_addr(&sm.c.scores));
             }
-            mma_arrive(smem_addr(&sm.c.scores));
-            wait(sm.c.weights, n);
+            __syncwarp();
+        };
+        scores(n);
+        for (int32_t j = 0; j < tiles; ++j, ++n) {
+            wait(sm.c.weights, n);             // the scores have been read, too
+            if (L::kApart && j + 1 < tiles) scores(n + 1);
             wait(sm.c.v_full, n);
+            __syncwarp();
             tmem_after();
+            if (one_lane()) {
 #pragma unroll
-            for (int s = 0; s < kTokens / 16; ++s)
-                mma_tmem(tmem + L::kSumsAt, tmem + L::kWeightsAt + 8 * s, operand(v + s * 16 * 128, 128 * 128),
-                         instruction(D, true), j > 0 || s > 0);
-            mma_arrive(smem_addr(&sm.c.summed));
+                for (int s = 0; s < kTokens / 16; ++s)
+                    mma_tmem(tmem + L::kSumsAt, tmem + L::kWeightsAt + s / 4 * L::kWeightsHalf + s % 4 * 8,
+                             v + ((s * 16 * 128) >> 4), instruction(D, true), j > 0 || s > 0);
+                mma_arrive(smem_addr(&sm.c.summed));
+            }
+            __syncwarp();
+            if (!L::kApart && j + 1 < tiles) { // the weights lie where the scores go
+                wait(sm.c.summed, n);
+                scores(n + 1);
+            }
         }
     }
 }
 
 // ---------------------------------------------------------------------------
 // the warps that own a query row a thread
+
+constexpr int kColumns = kTokens / 2;  // of a tile, for each thread of a row
 
 struct Pair {
     float x, y;
@@ -369,103 +411,179 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
-// What a pass over a row's scores finds.
-struct Found {
-    float most;          // the largest raw score
-    uint64_t sum;        // two sums of weights
-};
-
-// 16 columns of this row: their maximum, and with kWeights the weights
-// 2^(c s + against), written as fp16 pairs, and their sum.  Columns outside
-// [from, to) count as unseen.
-template <bool kEdge, bool kWeights>
-__device__ __forceinline__ void row_piece(float (&x)[16], int32_t q, uint32_t t_weights, int32_t from, int32_t to,
-                                          uint64_t c2, uint64_t against2, Found &f) {
-    if (kEdge) {
+// Columns outside [from, to) of 16 from column `at` count as unseen.
+__device__ __forceinline__ void hide(float (&x)[16], int32_t at, int32_t from, int32_t to) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (static_cast<uint32_t>(16 * q + i - from) >= static_cast<uint32_t>(to - from)) x[i] = -INFINITY;
-    }
-#pragma unroll
-    for (int i = 0; i < 16; i += 2) f.most = max3(f.most, x[i], x[i + 1]);
-    if (kWeights) {
-        uint32_t w[8];
-        uint64_t sum = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const Pair p = pair_of(fma_pair(bits_of(x[2 * i], x[2 * i + 1]), c2, against2));
-            const float a = exp2_fast(p.x), b = exp2_fast(p.y);
-            sum = add_pair(sum, bits_of(a, b));
-            w[i] = f16x2_of(a, b);
-        }
-        f.sum = add_pair(f.sum, sum);
-        tmem_store8(t_weights + 8 * q, w);
-    }
+    for (int i = 0; i < 16; ++i)
+        if (static_cast<uint32_t>(at + i - from) >= static_cast<uint32_t>(to - from)) x[i] = -INFINITY;
 }
 
-// One pass over the 128 scores of a row, 16 fetched while 16 are used.  A loop:
-// written out, its code did not stay in the instruction caches beside that of
-// the other warps (no instruction to issue for 2.6 cycles of each that was).
-template <bool kEdge, bool kWeights>
-__device__ __forceinline__ Found row_pass(uint32_t t_scores, uint32_t t_weights, int32_t from, int32_t to,
-                                          float c, float against) {
-    float x[16], y[16];
-    Found f = {-INFINITY, 0};
-    const uint64_t c2 = bits_of(c, c), against2 = bits_of(against, against);
-    tmem_load(t_scores, x);
-#pragma unroll 1
-    for (int32_t q = 0; q < kTokens / 16; q += 2) {
+// The largest of a thread's 64 scores of a row.
+template <bool kEdge>
+__device__ __forceinline__ float row_max(uint32_t t_scores, int32_t from, int32_t to) {
+    float x[2][16], most[2] = {-INFINITY, -INFINITY};
+    tmem_load(t_scores, x[0]);
+#pragma unroll
+    for (int q = 0; q < kColumns / 16; ++q) {
         tmem_wait_load();
-        tmem_load(t_scores + 16 * q + 16, y);
-        row_piece<kEdge, kWeights>(x, q, t_weights, from, to, c2, against2, f);
-        tmem_wait_load();
-        if (q + 2 < kTokens / 16) tmem_load(t_scores + 16 * q + 32, x);
-        row_piece<kEdge, kWeights>(y, q + 1, t_weights, from, to, c2, against2, f);
+        if (q + 1 < kColumns / 16) tmem_load(t_scores + 16 * (q + 1), x[(q + 1) % 2]);
+        if (kEdge) hide(x[q % 2], 16 * q, from, to);
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+            most[0] = max3(most[0], x[q % 2][i], x[q % 2][i + 1]);
+            most[1] = max3(most[1], x[q % 2][i + 2], x[q % 2][i + 3]);
+        }
     }
-    return f;
+    return fmaxf(most[0], most[1]);
+}
+
+// Their weights 2^(c s + against), written as fp16 pairs; returns the sum.
+template <bool kEdge>
+__device__ __forceinline__ float row_weights(uint32_t t_scores, uint32_t t_weights, int32_t from, int32_t to,
+                                             float c, float against) {
+    float x[2][16];
+    const uint64_t c2 = bits_of(c, c), against2 = bits_of(against, against);
+    uint64_t sum[2] = {0, 0};
+    tmem_load(t_scores, x[0]);
+#pragma unroll
+    for (int q = 0; q < kColumns / 16; ++q) {
+        tmem_wait_load();
+        if (q + 1 < kColumns / 16) tmem_load(t_scores + 16 * (q + 1), x[(q + 1) % 2]);
+        if (kEdge) hide(x[q % 2], 16 * q, from, to);
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const Pair p = pair_of(fma_pair(bits_of(x[q % 2][2 * i], x[q % 2][2 * i + 1]), c2, against2));
+            const float a = exp2_fast(p.x), b = exp2_fast(p.y);
+            sum[i % 2] = add_pair(sum[i % 2], bits_of(a, b));
+            w[i] = f16x2_of(a, b);
+        }
+        tmem_store8(t_weights + 8 * q, w);
+    }
+    const Pair p = pair_of(add_pair(sum[0], sum[1]));
+    return p.x + p.y;
+}
+
+// The two warps of 32 rows meet.
+__device__ __forceinline__ void pair_meet(int32_t quarter) {
+    asm volatile("bar.sync %0, 64;" :: "r"(quarter + 1) : "memory");
+}
+
+// What the other thread of this row has found.
+__device__ __forceinline__ float other_half(Control &c, int32_t half, int32_t row, float mine) {
+    c.halves[half][row] = mine;
+    pair_meet(row / 32);
+    const float v = c.halves[half ^ 1][row];
+    pair_meet(row / 32);                       // both have read
+    return v;
+}
+
+// A row of an item that is behind the products, for the output.
+struct Done {
+    RowPlace place;
+    int32_t part;        // as in Item; -2: nothing to put out
+    bool tiles;
+    float ref, sum;
+};
+
+template <int D>
+__device__ __forceinline__ void put_out(const Fp4Attention &a, const Done &done, uint32_t t_sums, int32_t half,
+                                        int32_t row, bool live, float v_scale) {
+    using L = Layout<D>;
+    float *part = part_at(a.workspace, 2 * static_cast<int64_t>(blockIdx.x) + max(done.part, 0), L::kPartFloats);
+    const float inv = row_factor(done.sum, v_scale);
+    uint4 *out = reinterpret_cast<uint4 *>(a.out + done.place.token * a.out_stride +
+                                           static_cast<int64_t>(done.place.q_head) * D);
+#pragma unroll 2
+    for (int q = half * (D / 32); q < (half + 1) * (D / 32); ++q) {
+        float o[16];
+        if (done.tiles) {
+            tmem_load(t_sums + 16 * q, o);
+            tmem_wait_load();
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = 0.0f;
+        }
+        if (done.part >= 0) {                          // [dimensions / 4][rows]
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                reinterpret_cast<float4 *>(part)[(4 * q + i) * kRows + row] =
+                    make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        } else if (live) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                out[2 * q + i] = make_uint4(bf16x2_of(o[8 * i] * inv, o[8 * i + 1] * inv),
+                                            bf16x2_of(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                            bf16x2_of(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                            bf16x2_of(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+        }
+    }
+    if (half == 0) {
+        if (done.part >= 0) {
+            part[kRows * D + row] = done.ref;
+            part[kRows * D + kRows + row] = done.sum;
+        } else if (live && a.lse != nullptr) {
+            a.lse[static_cast<int64_t>(done.place.token) * a.q_heads + done.place.q_head] =
+                row_lse(done.ref, done.sum, kShift);
+        }
+    }
+    tmem_before();                                     // the sums have been read
 }
 
 template <int D>
 __device__ __forceinline__ void softmax_items(const Fp4Attention &a, Shared<D> &sm, const Waits &wait,
                                               uint32_t tmem, int32_t group, float k_scale, float v_scale) {
     using L = Layout<D>;
-    const int32_t warp = threadIdx.x / 32, row = threadIdx.x;
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t t_scores = tmem + lanes, t_sums = t_scores + L::kSumsAt, t_weights = t_scores + L::kWeightsAt;
+    constexpr int kPieces = D / 16;                    // 16-byte pieces of half a query row
+    const int32_t half = threadIdx.x / 128, row = threadIdx.x % 128, quarter = row / 32;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t t_sums = tmem + lanes + L::kSumsAt;
+    const uint32_t t_scores = tmem + lanes + kColumns * half;
+    const uint32_t t_weights = tmem + lanes + L::kWeightsAt + L::kWeightsHalf * half;
     uint32_t n = 0;
+    Done done;
+    done.part = -2;
+    bool was_live = false;
     for (uint32_t items = 0;; ++items) {
         wait(sm.c.item_full[items % 2], items / 2);
         const Item it = sm.c.item[items % 2];
         warp_arrive(sm.c.item_empty[items % 2]);
-        if (it.tiles < 0) return;
-        const bool busy = warp * 32 < it.rows;         // the warp has rows
+        const bool busy = quarter * 32 < it.rows && it.tiles >= 0;   // the warp has rows
         const bool live = row < it.rows;
         const int32_t my_row = it.row0 + min(row, it.rows - 1);
         const RowPlace place = row_place(it.token0, my_row, it.head, group);
-        float c = 1.0f;                                // factor of raw scores: log2 of a weight
+        uint4 x[kPieces];                              // this half of the query row
         if (busy && it.tiles > 0) {
             const uint4 *src = reinterpret_cast<const uint4 *>(
-                a.q + place.token * a.q_stride + static_cast<int64_t>(place.q_head) * D);
+                a.q + place.token * a.q_stride + static_cast<int64_t>(place.q_head) * D) + half * kPieces;
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) x[i] = src[i];
+        }
+        // The last item's output, while the query rows come.
+        if (done.part > -2) put_out<D>(a, done, t_sums, half, row, was_live, v_scale);
+        if (it.tiles < 0) return;
+        done.part = -2;
+        was_live = live;
+        float c = 1.0f;                                // factor of raw scores: log2 of a weight
+        if (busy && it.tiles > 0) {
             uint32_t most = 0;
-#pragma unroll 8
-            for (int i = 0; i < D / 8; ++i) {
-                const uint4 x = src[i];
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) most = max(most, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
             }
+            most = max(most, __float_as_uint(other_half(sm.c, half, row, __uint_as_float(most))));
             const int32_t up = min(8 - (static_cast<int32_t>(most >> 7) - 127), 120);
             const float scale = live ? __int_as_float((127 + up) << 23) : 0.0f;
             c = fmaxf(a.softmax_scale * kLog2e * k_scale * __int_as_float((127 - up) << 23), 0x1p-100f);
-#pragma unroll 4
-            for (int i = 0; i < D / 8; ++i) {
-                const uint4 x = src[i];
-                *reinterpret_cast<uint4 *>(sm.q + piece_at(row, i)) =
-                    make_uint4(f16x2_of(bf16_low(x.x) * scale, bf16_high(x.x) * scale),
-                               f16x2_of(bf16_low(x.y) * scale, bf16_high(x.y) * scale),
-                               f16x2_of(bf16_low(x.z) * scale, bf16_high(x.z) * scale),
-                               f16x2_of(bf16_low(x.w) * scale, bf16_high(x.w) * scale));
-            }
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i)
+                *reinterpret_cast<uint4 *>(sm.q + piece_at(row, half * kPieces + i)) =
+                    make_uint4(f16x2_of(bf16_low(x[i].x) * scale, bf16_high(x[i].x) * scale),
+                               f16x2_of(bf16_low(x[i].y) * scale, bf16_high(x[i].y) * scale),
+                               f16x2_of(bf16_low(x[i].z) * scale, bf16_high(x[i].z) * scale),
+                               f16x2_of(bf16_low(x[i].w) * scale, bf16_high(x[i].w) * scale));
         }
         if (it.tiles > 0) {
             operands_written();
@@ -477,99 +595,65 @@ __device__ __forceinline__ void softmax_items(const Fp4Attention &a, Shared<D> &
         const int32_t all_hi = __reduce_min_sync(0xFFFFFFFFu, hi), all_lo = __reduce_max_sync(0xFFFFFFFFu, lo);
         float ref = -INFINITY, sum = 0.0f;
         for (int32_t j = 0; j < it.tiles; ++j, ++n) {
-            if (n > 0) wait(sm.c.summed, n - 1);
             wait(sm.c.scores, n);
             __syncwarp();
             tmem_after();
+            // the last product is done: sums may be rescaled, weights replaced
+            bool waited = n == 0;
+            auto summed = [&]() {
+                if (!waited) wait(sm.c.summed, n - 1);
+                waited = true;
+                __syncwarp();
+                tmem_after();
+            };
+            if (!busy) summed();
             if (busy) {
                 const int32_t base = it.begin + j * kTokens;
                 const bool edge = base + kTokens > all_hi || base < all_lo;
-                const int32_t from = lo - base, to = max(from, hi - base);   // columns this row sees
-                // Moves the reference where a row of the warp has outgrown it.
-                auto follow = [&](float top) -> bool {
-                    if (!__any_sync(0xFFFFFFFFu, top > ref + kSlack)) return false;
+                // columns this row sees, of this thread's
+                const int32_t from = lo - base - kColumns * half, to = max(from, hi - base - kColumns * half);
+                float top = edge ? row_max<true>(t_scores, from, to) : row_max<false>(t_scores, from, to);
+                top = fmaxf(top, other_half(sm.c, half, row, top)) * c;
+                // The reference moves where a row of the warps has outgrown it.
+                if (__any_sync(0xFFFFFFFFu, top > ref + kSlack)) {
                     const float now = fmaxf(ref, top);
                     const float f = exp2_fast(ref - (now == -INFINITY ? 0.0f : now));
                     ref = now;
                     sum *= f;
                     if (j > 0) {
+                        summed();
 #pragma unroll 1
-                        for (int q = 0; q < D / 16; ++q) {
+                        for (int q = half * (D / 32); q < (half + 1) * (D / 32); ++q) {
                             float o[16];
                             tmem_load(t_sums + 16 * q, o);
                             tmem_wait_load();
 #pragma unroll
                             for (int i = 0; i < 16; ++i) o[i] *= f;
-                            tmem_store16(t_sums + 16 * q, o);
+                            tmem_store(t_sums + 16 * q, o);
                         }
                     }
-                    return true;
-                };
-                // Behind the first tile the maximum is found together with the
-                // weights, and these are made again where it had grown; where
-                // they replace the scores it has to come first.
-                const bool max_first = !L::kApart || j == 0;
-                if (max_first) {
-                    const Found f = edge ? row_pass<true, false>(t_scores, 0, from, to, c, 0.0f)
-                                         : row_pass<false, false>(t_scores, 0, from, to, c, 0.0f);
-                    follow(f.most * c);
                 }
-                Found f;
-                do {
-                    const float against = kShift - (ref == -INFINITY ? 0.0f : ref);
-                    f = edge ? row_pass<true, true>(t_scores, t_weights, from, to, c, against)
-                             : row_pass<false, true>(t_scores, t_weights, from, to, c, against);
-                } while (!max_first && follow(f.most * c));
-                const Pair add = pair_of(f.sum);
-                sum += add.x + add.y;
+                const float against = kShift - (ref == -INFINITY ? 0.0f : ref);
+                summed();
+                sum += edge ? row_weights<true>(t_scores, t_weights, from, to, c, against)
+                            : row_weights<false>(t_scores, t_weights, from, to, c, against);
                 tmem_wait_store();
             }
             tmem_before();
             warp_arrive(sm.c.weights);
         }
-
-        // ---- output ----------------------------------------------------------
         if (it.tiles > 0) {
             wait(sm.c.summed, n - 1);
             __syncwarp();
             tmem_after();
         }
         if (!busy) continue;
-        float *part = part_at(a.workspace, 2 * static_cast<int64_t>(blockIdx.x) + max(it.part, 0), L::kPartFloats);
-        const float inv = row_factor(sum, v_scale);
-        uint4 *out = reinterpret_cast<uint4 *>(a.out + place.token * a.out_stride +
-                                               static_cast<int64_t>(place.q_head) * D);
-#pragma unroll 1
-        for (int q = 0; q < D / 16; ++q) {
-            float o[16];
-            if (it.tiles > 0) {
-                tmem_load(t_sums + 16 * q, o);
-                tmem_wait_load();
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = 0.0f;
-            }
-            if (it.part >= 0) {                        // [dimensions / 4][rows]
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    reinterpret_cast<float4 *>(part)[(4 * q + i) * kRows + row] =
-                        make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-            } else if (live) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    out[2 * q + i] = make_uint4(bf16x2_of(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                                bf16x2_of(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                                bf16x2_of(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                                bf16x2_of(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
-            }
-        }
-        if (it.part >= 0) {
-            part[kRows * D + row] = ref;
-            part[kRows * D + kRows + row] = sum;
-        } else if (live && a.lse != nullptr) {
-            a.lse[static_cast<int64_t>(place.token) * a.q_heads + place.q_head] = row_lse(ref, sum, kShift);
-        }
-        tmem_before();                                 // the sums have been read
+        sum += other_half(sm.c, half, row, sum);
+        done.place = place;
+        done.part = it.part;
+        done.tiles = it.tiles > 0;
+        done.ref = ref;
+        done.sum = sum;
     }
 }
 
@@ -577,7 +661,7 @@ __device__ __forceinline__ void softmax_items(const Fp4Attention &a, Shared<D> &
 // the kernel
 
 // Moves registers between the warp groups of a block: with two blocks on an SM
-// a thread starts with 80, and 112 + 72 + 56 are three times that.
+// a thread starts with 64, and 72 + 72 + 72 + 40 are four times that.
 template <bool kMove, int kCount, bool kMore>
 __device__ __forceinline__ void registers() {
     if constexpr (kMove && kMore) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kCount));
@@ -592,9 +676,9 @@ __global__ void __launch_bounds__(kThreads, Layout<D>::kBlocks) fp4_attention_ro
     Shared<D> &sm = *reinterpret_cast<Shared<D> *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) / 1024 * 1024);   // the swizzle goes by the address
     Control &c = sm.c;
-    const int32_t warp = threadIdx.x / 32;
+    const int32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x / 32, 0);
     const Division d = {a.q_heads / a.pools.heads, kRows, a.pools.heads, kTokens, a.window, whole};
-    if (warp == 8)
+    if (warp == kIssueThread / 32)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n\t"
                      "tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;"
                      :: "r"(smem_addr(&c.tmem)), "n"(L::kColumns) : "memory");
@@ -602,13 +686,13 @@ __global__ void __launch_bounds__(kThreads, Layout<D>::kBlocks) fp4_attention_ro
         c.gave_up = 0;
         for (int i = 0; i < 2; ++i) {
             barrier_init(smem_addr(&c.item_full[i]), 1);
-            barrier_init(smem_addr(&c.item_empty[i]), 9);    // eight warps and the issuing thread
+            barrier_init(smem_addr(&c.item_empty[i]), 13);   // twelve warps and the issuing one
         }
-        barrier_init(smem_addr(&c.q_full), 4);
+        barrier_init(smem_addr(&c.q_full), 8);
         barrier_init(smem_addr(&c.k_full), 4);
         barrier_init(smem_addr(&c.v_full), 4);
         barrier_init(smem_addr(&c.scores), 1);
-        barrier_init(smem_addr(&c.weights), 4);
+        barrier_init(smem_addr(&c.weights), 8);
         barrier_init(smem_addr(&c.summed), 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -622,22 +706,22 @@ __global__ void __launch_bounds__(kThreads, Layout<D>::kBlocks) fp4_attention_ro
     tmem_before();
     const Run run = block_run<kThreads / 32>(a, d, &g_fp4_rows_error, c.plan);   // a block barrier at least
     tmem_after();
-    const uint32_t tmem = c.tmem;
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, c.tmem, 0);
     const bool scales_ok = fp4_scale_ok(k_scale) && fp4_scale_ok(v_scale);
     if (!scales_ok && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_fp4_rows_error, kFp4ErrScale);
     if (scales_ok && run.at < run.end) {
         const Waits wait{c};
-        if (warp < 4) {
-            registers<L::kBlocks == 2, 112, true>();
+        if (threadIdx.x < kTokenThread) {
+            registers<L::kBlocks == 2, 72, true>();
             softmax_items<D>(a, sm, wait, tmem, d.group, k_scale, v_scale);
-        } else if (warp < 8) {
-            registers<L::kBlocks == 2, 72, false>();
+        } else if (threadIdx.x < kIssueThread) {
+            registers<L::kBlocks == 2, 72, true>();
             expand_items<D>(a, sm, wait);
         } else {
-            registers<L::kBlocks == 2, 56, false>();
-            if (threadIdx.x == 256)
+            registers<L::kBlocks == 2, 40, false>();
+            if (warp == kIssueThread / 32)
                 issue_items<D>(sm, wait, tmem);
-            else if (warp == 9)
+            else if (warp == kIssueThread / 32 + 1)
                 walk_items(a, c, wait, run, d, record);
         }
     }
@@ -645,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D>::kBlocks) fp4_attention_ro
     tmem_before();
     __syncthreads();
     if (*static_cast<volatile uint32_t *>(&c.gave_up)) __nanosleep(1000000);   // products under way end
-    if (warp == 8) {
+    if (warp == kIssueThread / 32) {
         tmem_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "n"(L::kColumns));
     }
