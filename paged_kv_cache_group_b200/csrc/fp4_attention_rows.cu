@@ -266,51 +266,38 @@ __device__ __forceinline__ void expand_items(const Fp4Attention &a, Shared<D> &s
                 page = 0;
             }
             const int64_t tile = page * a.pools.block_stride + (head + (at16 - page_at * tiles)) * (9 * D);
-            const uint8_t *kt = a.pools.k + tile, *vt = a.pools.v + tile;
-            uint2 kc[kBlocks16], vc[kBlocks16];
-            uint32_t kz[kBlocks16 / 4], vz[kBlocks16];
-#pragma unroll
-            for (int b = 0; b < kBlocks16; b += 2) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(kt + slot * (D / 2) + 8 * b);
-                kc[b] = make_uint2(x.x, x.y), kc[b + 1] = make_uint2(x.z, x.w);
-            }
-#pragma unroll
-            for (int b = 0; b < kBlocks16 / 4; ++b) {
-                kz[b] = *reinterpret_cast<const uint32_t *>(kt + 8 * D + slot * kBlocks16 + 4 * b);
-                if (mine != tok) kz[b] = 0;
-            }
-            auto load_v = [&]() {
+            // K, then V: one code for both, that it stays in the instruction caches.
+#pragma unroll 1
+            for (int32_t of_v = 0; of_v < 2; ++of_v) {
+                const uint8_t *pool = of_v ? a.pools.v + tile : a.pools.k + tile;
+                const uint8_t *code = pool + slot * (of_v ? 8 : D / 2);
+                const uint8_t *scale = pool + 8 * D + slot * (of_v ? 1 : kBlocks16);
+                const int32_t code_step = of_v ? 128 : 8, scale_step = of_v ? 16 : 1;
+                uint2 codes[kBlocks16];
+                uint32_t scales[kBlocks16];
 #pragma unroll
                 for (int b = 0; b < kBlocks16; ++b) {
-                    vc[b] = *reinterpret_cast<const uint2 *>(vt + b * 128 + slot * 8);
-                    vz[b] = vt[8 * D + b * 16 + slot];
-                    if (mine != tok) vz[b] = 0;
+                    codes[b] = *reinterpret_cast<const uint2 *>(code + b * code_step);
+                    scales[b] = scale[b * scale_step];
                 }
-            };
-            if (D != 128) load_v();            // at once where there are registers for both
-            // `scale`: a block's scale byte twice
-            auto write = [&](uint8_t *dst, int b, uint2 codes, uint32_t scale) {
-                const uint32_t s = f16x2_of_e4m3x2(scale);
-                uint32_t x[4];
+                // the last product with this operand is done
+                if (n > 0) wait(of_v ? sm.c.summed : sm.c.scores, n - 1);
+                uint8_t *dst = of_v ? sm.v : sm.k;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    f16x2_of_e2m1x8(h ? codes.y : codes.x, x);
-                    const int c = 2 * b + h;
-                    *reinterpret_cast<uint4 *>(dst + c / 8 * (128 * 128) + (at_row ^ (c % 8 * 16))) =
-                        make_uint4(mul_f16x2(x[0], s), mul_f16x2(x[1], s), mul_f16x2(x[2], s), mul_f16x2(x[3], s));
+                for (int b = 0; b < kBlocks16; ++b) {
+                    const uint32_t s = f16x2_of_e4m3x2(mine == tok ? scales[b] * 0x101u : 0);
+                    uint32_t x[4];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        f16x2_of_e2m1x8(h ? codes[b].y : codes[b].x, x);
+                        const int c = 2 * b + h;
+                        *reinterpret_cast<uint4 *>(dst + c / 8 * (128 * 128) + (at_row ^ (c % 8 * 16))) =
+                            make_uint4(mul_f16x2(x[0], s), mul_f16x2(x[1], s), mul_f16x2(x[2], s), mul_f16x2(x[3], s));
+                    }
                 }
-            };
-            if (n > 0) wait(sm.c.scores, n - 1);       // the last product with K is done
-#pragma unroll
-            for (int b = 0; b < kBlocks16; ++b) write(sm.k, b, kc[b], __byte_perm(kz[b / 4], 0, 0x11 * (b % 4)));
-            operands_written();
-            warp_arrive(sm.c.k_full);
-            if (D == 128) load_v();
-            if (n > 0) wait(sm.c.summed, n - 1);       // ... and with V
-#pragma unroll
-            for (int b = 0; b < kBlocks16; ++b) write(sm.v, b, vc[b], vz[b] * 0x101u);
-            operands_written();
-            warp_arrive(sm.c.v_full);
+                operands_written();
+                warp_arrive(of_v ? sm.c.v_full : sm.c.k_full);
+            }
         }
     }
 }
@@ -340,8 +327,7 @@ __device__ __forceinline__ void issue_items(Shared<D> &sm, const Waits &wait, ui
         if (tiles < 0) return;
         if (tiles == 0) continue;
         wait(sm.c.q_full, full++);
-        auto scores = [&](uint32_t at) {       // S of a tile
-            wait(sm.c.k_full, at);
+        auto scores = [&]() {                  // S of a tile
             __syncwarp();
             tmem_after();
             if (one_lane()) {
@@ -354,11 +340,14 @@ __device__ __forceinline__ void issue_items(Shared<D> &sm, const Waits &wait, ui
             }
             __syncwarp();
         };
-        scores(n);
+        wait(sm.c.k_full, n);
+        scores();
         for (int32_t j = 0; j < tiles; ++j, ++n) {
-            wait(sm.c.weights, n);             // the scores have been read, too
-            if (L::kApart && j + 1 < tiles) scores(n + 1);
+            // The weights come last; nothing else is waited for behind them.
+            if (j + 1 < tiles) wait(sm.c.k_full, n + 1);
             wait(sm.c.v_full, n);
+            wait(sm.c.weights, n);             // the scores have been read, too
+            if (L::kApart && j + 1 < tiles) scores();
             __syncwarp();
             tmem_after();
             if (one_lane()) {
@@ -371,7 +360,7 @@ __device__ __forceinline__ void issue_items(Shared<D> &sm, const Waits &wait, ui
             __syncwarp();
             if (!L::kApart && j + 1 < tiles) { // the weights lie where the scores go
                 wait(sm.c.summed, n);
-                scores(n + 1);
+                scores();
             }
         }
     }
@@ -661,7 +650,7 @@ __device__ __forceinline__ void softmax_items(const Fp4Attention &a, Shared<D> &
 // the kernel
 
 // Moves registers between the warp groups of a block: with two blocks on an SM
-// a thread starts with 64, and 72 + 72 + 72 + 40 are four times that.
+// a thread starts with 64, and 72 + 72 + 56 + 56 are four times that.
 template <bool kMove, int kCount, bool kMore>
 __device__ __forceinline__ void registers() {
     if constexpr (kMove && kMore) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kCount));
@@ -715,10 +704,10 @@ __global__ void __launch_bounds__(kThreads, Layout<D>::kBlocks) fp4_attention_ro
             registers<L::kBlocks == 2, 72, true>();
             softmax_items<D>(a, sm, wait, tmem, d.group, k_scale, v_scale);
         } else if (threadIdx.x < kIssueThread) {
-            registers<L::kBlocks == 2, 72, true>();
+            registers<L::kBlocks == 2, 56, false>();
             expand_items<D>(a, sm, wait);
         } else {
-            registers<L::kBlocks == 2, 40, false>();
+            registers<L::kBlocks == 2, 56, false>();
             if (warp == kIssueThread / 32)
                 issue_items<D>(sm, wait, tmem);
             else if (warp == kIssueThread / 32 + 1)

@@ -12,7 +12,10 @@
 // 9/16 byte of cache on the other, with about two instructions an element.
 // One thread owns one 16-element block of K and the same block of V: four
 // 16-byte accesses in flight on the bf16 side, an 8-byte code word and a
-// scale byte on the cache side, and no exchange between threads.
+// scale byte on the cache side, and no exchange between threads.  A warp takes
+// one head of four neighbouring tokens (eight with 64 dimensions), so that V's
+// code words, which lie by block and then by token, fill whole sectors: one
+// token a warp asked for four times the sectors.
 #include <cuda_runtime.h>
 
 #include "fp4_device.cuh"
@@ -36,7 +39,13 @@ template <int D>
 __device__ __forceinline__ BlockPlace block_place(const Fp4Pools &p, int64_t slot, int32_t head,
                                                   int32_t block) {
     const int32_t block_size = p.tiles * 16;
-    const int64_t page = slot / block_size;
+    int64_t page;
+    if ((block_size & (block_size - 1)) == 0)
+        page = slot >> (__ffs(block_size) - 1);
+    else if (slot >> 32 == 0)
+        page = static_cast<uint32_t>(slot) / static_cast<uint32_t>(block_size);
+    else
+        page = slot / block_size;
     const int32_t off = static_cast<int32_t>(slot - page * block_size);
     const uint32_t tok = off & 15;
     BlockPlace b;
@@ -48,15 +57,28 @@ __device__ __forceinline__ BlockPlace block_place(const Fp4Pools &p, int64_t slo
     return b;
 }
 
-// Block index -> (token, head, block of the head).
+// The work of a thread: a warp is kTokens tokens x kAcross blocks of one head.
 template <int D>
-__device__ __forceinline__ void split_index(uint32_t i, int32_t heads, uint32_t *token,
-                                            int32_t *head, int32_t *block) {
-    const uint32_t row = i / (D / 16);
-    *block = static_cast<int32_t>(i % (D / 16));
-    *token = row / static_cast<uint32_t>(heads);
-    *head = static_cast<int32_t>(row - *token * static_cast<uint32_t>(heads));
-}
+struct Share {
+    static constexpr int kBlocks = D / 16;
+    static constexpr int kAcross = kBlocks < 8 ? kBlocks : 8;
+    static constexpr int kTokens = 32 / kAcross;
+    static constexpr int kParts = kBlocks / kAcross;    // warps of a head's tokens
+    uint32_t token;
+    int32_t head, block;
+
+    __device__ __forceinline__ explicit Share(int32_t heads) {
+        const uint32_t warp = blockIdx.x * (kThreads / 32) + threadIdx.x / 32, lane = threadIdx.x % 32;
+        const uint32_t row = warp / kParts;             // (token group, head)
+        const uint32_t group = row / static_cast<uint32_t>(heads);
+        token = group * kTokens + lane / kAcross;
+        head = static_cast<int32_t>(row - group * static_cast<uint32_t>(heads));
+        block = static_cast<int32_t>(warp % kParts * kAcross + lane % kAcross);
+    }
+    static int64_t warps(int64_t tokens, int64_t heads) {
+        return (tokens + kTokens - 1) / kTokens * heads * kParts;
+    }
+};
 
 __device__ __forceinline__ void load_scales(const Fp4Pools &p, float *ks, float *vs) {
     *ks = p.scale_dev ? p.scale_dev[0] : p.k_scale;
@@ -96,28 +118,25 @@ __device__ __forceinline__ uint2 quantise16(const uint4 &a, const uint4 &b, floa
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) fp4_write_kernel(const Fp4Rows r, const Fp4Pools p,
-                                                             uint32_t blocks) {
+__global__ void __launch_bounds__(kThreads) fp4_write_kernel(const Fp4Rows r, const Fp4Pools p) {
     pdl_wait();
     pdl_allow_next();
-    const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
-    if (i >= blocks) return;
-    uint32_t token;
-    int32_t head, block;
-    split_index<D>(i, p.heads, &token, &head, &block);
-    const int64_t slot = r.slots[token];
+    const Share<D> me(p.heads);
+    if (me.token >= r.num_tokens) return;
+    // the rows do not wait for the slot
+    const int64_t slot = r.slots[me.token];
+    const int32_t e = me.head * D + me.block * 16;
+    const uint4 *k = reinterpret_cast<const uint4 *>(r.k + me.token * r.key_stride + e);
+    const uint4 *v = reinterpret_cast<const uint4 *>(r.v + me.token * r.value_stride + e);
+    const uint4 k0 = __ldcs(k), k1 = __ldcs(k + 1), v0 = __ldcs(v), v1 = __ldcs(v + 1);
+    float ks, vs;
+    load_scales(p, &ks, &vs);
     if (slot < 0) return;
     if (slot >= p.num_blocks * (p.tiles * 16)) {
         atomicOr(&g_fp4_kv_error, kFp4ErrSlot);
         return;
     }
-    const int32_t e = head * D + block * 16;
-    const uint4 *k = reinterpret_cast<const uint4 *>(r.k + token * r.key_stride + e);
-    const uint4 *v = reinterpret_cast<const uint4 *>(r.v + token * r.value_stride + e);
-    const uint4 k0 = __ldcs(k), k1 = __ldcs(k + 1), v0 = __ldcs(v), v1 = __ldcs(v + 1);
-    float ks, vs;
-    load_scales(p, &ks, &vs);
-    const BlockPlace at = block_place<D>(p, slot, head, block);
+    const BlockPlace at = block_place<D>(p, slot, me.head, me.block);
     const bool k_ok = fp4_scale_ok(ks), v_ok = fp4_scale_ok(vs);
     if (!k_ok || !v_ok) atomicOr(&g_fp4_kv_error, kFp4ErrScale);
     uint32_t sc;
@@ -155,22 +174,18 @@ __device__ __forceinline__ void dequantise16(uint2 codes, uint32_t scale_code, f
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) fp4_read_kernel(const Fp4Rows r, const Fp4Pools p,
-                                                            uint32_t blocks) {
+__global__ void __launch_bounds__(kThreads) fp4_read_kernel(const Fp4Rows r, const Fp4Pools p) {
     pdl_wait();
     pdl_allow_next();
-    const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
-    if (i >= blocks) return;
-    uint32_t token;
-    int32_t head, block;
-    split_index<D>(i, p.heads, &token, &head, &block);
-    const int64_t slot = r.slots[token];
+    const Share<D> me(p.heads);
+    if (me.token >= r.num_tokens) return;
+    const int64_t slot = r.slots[me.token];
     if (slot < 0) return;
     if (slot >= p.num_blocks * (p.tiles * 16)) {
         atomicOr(&g_fp4_kv_error, kFp4ErrSlot);
         return;
     }
-    const BlockPlace at = block_place<D>(p, slot, head, block);
+    const BlockPlace at = block_place<D>(p, slot, me.head, me.block);
     const uint2 kc = *reinterpret_cast<const uint2 *>(p.k + at.tile + at.k_code);
     const uint2 vc = *reinterpret_cast<const uint2 *>(p.v + at.tile + at.v_code);
     const uint32_t kb = p.k[at.tile + at.k_scale], vb = p.v[at.tile + at.v_scale];
@@ -178,38 +193,39 @@ __global__ void __launch_bounds__(kThreads) fp4_read_kernel(const Fp4Rows r, con
     load_scales(p, &ks, &vs);
     const bool k_ok = fp4_scale_ok(ks), v_ok = fp4_scale_ok(vs);
     if (!k_ok || !v_ok) atomicOr(&g_fp4_kv_error, kFp4ErrScale);
-    const int32_t e = head * D + block * 16;
+    const int32_t e = me.head * D + me.block * 16;
     uint4 a, b;
     if (k_ok) {
         dequantise16(kc, kb, ks, &a, &b);
-        uint4 *k = reinterpret_cast<uint4 *>(r.k + token * r.key_stride + e);
+        uint4 *k = reinterpret_cast<uint4 *>(r.k + me.token * r.key_stride + e);
         k[0] = a;
         k[1] = b;
     }
     if (v_ok) {
         dequantise16(vc, vb, vs, &a, &b);
-        uint4 *v = reinterpret_cast<uint4 *>(r.v + token * r.value_stride + e);
+        uint4 *v = reinterpret_cast<uint4 *>(r.v + me.token * r.value_stride + e);
         v[0] = a;
         v[1] = b;
     }
 }
 
-// Block indexes are 32 bits inside a launch; more tokens than that take
+// Thread indexes are 32 bits inside a launch; more tokens than that take
 // several launches.
-template <typename Kernel>
+template <int D, typename Kernel>
 cudaError_t launch_rows(Kernel kernel, Fp4Rows r, const Fp4Pools &p, cudaStream_t stream) {
-    const int64_t per_token = static_cast<int64_t>(p.heads) * (p.dim / 16);
-    const int64_t most = (int64_t{1} << 30) / per_token;
-    while (r.num_tokens > 0) {
-        const int64_t n = r.num_tokens < most ? r.num_tokens : most;
-        const uint32_t blocks = static_cast<uint32_t>(n * per_token);
-        const cudaError_t e = launch_pdl(kernel, dim3((blocks + kThreads - 1) / kThreads), kThreads,
-                                         0, stream, r, p, blocks);
+    const int64_t most = (int64_t{1} << 25) / (static_cast<int64_t>(p.heads) * Share<D>::kParts) *
+                         Share<D>::kTokens;            // a multiple of a warp's tokens
+    const int64_t all = r.num_tokens;
+    for (int64_t done = 0; done < all; done += most) {
+        Fp4Rows part = r;
+        part.num_tokens = all - done < most ? all - done : most;
+        part.k += done * r.key_stride;
+        part.v += done * r.value_stride;
+        part.slots += done;
+        const int64_t warps = Share<D>::warps(part.num_tokens, p.heads);
+        const cudaError_t e = launch_pdl(kernel, dim3(static_cast<unsigned>((warps * 32 + kThreads - 1) / kThreads)),
+                                         kThreads, 0, stream, part, p);
         if (e != cudaSuccess) return e;
-        r.num_tokens -= n;
-        r.k += n * r.key_stride;
-        r.v += n * r.value_stride;
-        r.slots += n;
     }
     return cudaSuccess;
 }
@@ -217,17 +233,15 @@ cudaError_t launch_rows(Kernel kernel, Fp4Rows r, const Fp4Pools &p, cudaStream_
 }  // namespace
 
 cudaError_t launch_fp4_write(const Fp4Rows &r, const Fp4Pools &p, cudaStream_t stream) {
-    return launch_rows(p.dim == 64    ? fp4_write_kernel<64>
-                       : p.dim == 128 ? fp4_write_kernel<128>
-                                      : fp4_write_kernel<256>,
-                       r, p, stream);
+    return p.dim == 64    ? launch_rows<64>(fp4_write_kernel<64>, r, p, stream)
+           : p.dim == 128 ? launch_rows<128>(fp4_write_kernel<128>, r, p, stream)
+                          : launch_rows<256>(fp4_write_kernel<256>, r, p, stream);
 }
 
 cudaError_t launch_fp4_read(const Fp4Rows &r, const Fp4Pools &p, cudaStream_t stream) {
-    return launch_rows(p.dim == 64    ? fp4_read_kernel<64>
-                       : p.dim == 128 ? fp4_read_kernel<128>
-                                      : fp4_read_kernel<256>,
-                       r, p, stream);
+    return p.dim == 64    ? launch_rows<64>(fp4_read_kernel<64>, r, p, stream)
+           : p.dim == 128 ? launch_rows<128>(fp4_read_kernel<128>, r, p, stream)
+                          : launch_rows<256>(fp4_read_kernel<256>, r, p, stream);
 }
 
 cudaError_t read_fp4_kv_error(uint32_t *bits, bool clear) {

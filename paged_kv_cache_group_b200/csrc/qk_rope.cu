@@ -67,58 +67,69 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const QkNormRope
     const LanePlace at = lane_place<kInterleaved>(lane, p.rotary);
     const int32_t heads = p.q_heads + p.k_heads;
     const int32_t items = tokens * heads;
-    // Every thread of a warp runs the same number of passes, for the shuffles.
+    // Every thread of a warp runs the same number of passes, for the shuffles;
+    // a pass is kUnroll heads, all fetched before the first is used.
+    constexpr int kUnroll = 4;
     const int32_t step = kGroups * parts;
-    for (int32_t base = part * kGroups; base < items; base += step) {
-        const int32_t item = base + threadIdx.x / kLanes;
-        const bool live = item < items;
-        const int32_t t = live ? item / heads : 0;
-        const int32_t h = live ? item - t * heads : 0;
-        const bool is_q = h < p.q_heads;
-        const int64_t row = t0 + t;
-        const int32_t head = is_q ? h : h - p.q_heads;
-        const uint16_t *src = (is_q ? p.q + row * p.q_stride : p.k + row * p.k_stride) + head * D;
-        uint16_t *dst = (is_q ? p.q_out + row * p.q_out_stride : p.k_out + row * p.k_out_stride) + head * D;
-        const uint16_t *weight = is_q ? p.q_weight : p.k_weight;
-        float x[8];
-        {
-            uint2 a = make_uint2(0, 0), b = a;
-            if (live) {
-                a = *reinterpret_cast<const uint2 *>(src + at.first);
-                b = *reinterpret_cast<const uint2 *>(src + at.second);
-            }
-            x[0] = bf16_low(a.x), x[1] = bf16_high(a.x), x[2] = bf16_low(a.y), x[3] = bf16_high(a.y);
-            x[4] = bf16_low(b.x), x[5] = bf16_high(b.x), x[6] = bf16_low(b.y), x[7] = bf16_high(b.y);
-        }
-        float sum = 0.0f;
+    for (int32_t base = part * kGroups; base < items; base += kUnroll * step) {
+        uint2 first[kUnroll], second[kUnroll];
+        uint16_t *dst[kUnroll];
+        int32_t token[kUnroll];                 // in the block; -1: no item
+        bool is_q[kUnroll];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        if (!live) continue;
-        if (weight != nullptr) {
-            const float n = rsqrtf(sum * (1.0f / D) + p.eps);
-            const uint2 a = *reinterpret_cast<const uint2 *>(weight + at.first);
-            const uint2 b = *reinterpret_cast<const uint2 *>(weight + at.second);
-            const float w[8] = {bf16_low(a.x), bf16_high(a.x), bf16_low(a.y), bf16_high(a.y),
-                                bf16_low(b.x), bf16_high(b.x), bf16_low(b.y), bf16_high(b.y)};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = x[i] * n * w[i];
-        }
-        if (at.pair >= 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 cs = turns[t][at.pair + i];
-                const int u = kInterleaved ? 2 * i : i, v = kInterleaved ? 2 * i + 1 : i + 4;
-                const float a = x[u], b = x[v];
-                x[u] = a * cs.x - b * cs.y;
-                x[v] = b * cs.x + a * cs.y;
+        for (int u = 0; u < kUnroll; ++u) {
+            const int32_t item = base + u * step + threadIdx.x / kLanes;
+            first[u] = second[u] = make_uint2(0, 0);
+            token[u] = -1;
+            if (item < items) {
+                const int32_t t = tokens == 1 ? 0 : item / heads, h = item - t * heads;
+                is_q[u] = h < p.q_heads;
+                const int64_t row = t0 + t;
+                const int32_t head = is_q[u] ? h : h - p.q_heads;
+                const uint16_t *src =
+                    (is_q[u] ? p.q + row * p.q_stride : p.k + row * p.k_stride) + head * D;
+                dst[u] = (is_q[u] ? p.q_out + row * p.q_out_stride : p.k_out + row * p.k_out_stride) + head * D;
+                token[u] = t;
+                first[u] = *reinterpret_cast<const uint2 *>(src + at.first);
+                second[u] = *reinterpret_cast<const uint2 *>(src + at.second);
             }
         }
-        *reinterpret_cast<uint2 *>(dst + at.first) =
-            make_uint2(bf16x2_of(x[0], x[1]), bf16x2_of(x[2], x[3]));
-        *reinterpret_cast<uint2 *>(dst + at.second) =
-            make_uint2(bf16x2_of(x[4], x[5]), bf16x2_of(x[6], x[7]));
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const uint2 a = first[u], b = second[u];
+            float x[8] = {bf16_low(a.x), bf16_high(a.x), bf16_low(a.y), bf16_high(a.y),
+                          bf16_low(b.x), bf16_high(b.x), bf16_low(b.y), bf16_high(b.y)};
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+            if (token[u] < 0) continue;
+            const uint16_t *weight = is_q[u] ? p.q_weight : p.k_weight;
+            if (weight != nullptr) {
+                const float n = rsqrtf(sum * (1.0f / D) + p.eps);
+                const uint2 wa = *reinterpret_cast<const uint2 *>(weight + at.first);
+                const uint2 wb = *reinterpret_cast<const uint2 *>(weight + at.second);
+                const float w[8] = {bf16_low(wa.x), bf16_high(wa.x), bf16_low(wa.y), bf16_high(wa.y),
+                                    bf16_low(wb.x), bf16_high(wb.x), bf16_low(wb.y), bf16_high(wb.y)};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = x[i] * n * w[i];
+            }
+            if (at.pair >= 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 cs = turns[token[u]][at.pair + i];
+                    const int s = kInterleaved ? 2 * i : i, v = kInterleaved ? 2 * i + 1 : i + 4;
+                    const float c = x[s], e = x[v];
+                    x[s] = c * cs.x - e * cs.y;
+                    x[v] = e * cs.x + c * cs.y;
+                }
+            }
+            *reinterpret_cast<uint2 *>(dst[u] + at.first) =
+                make_uint2(bf16x2_of(x[0], x[1]), bf16x2_of(x[2], x[3]));
+            *reinterpret_cast<uint2 *>(dst[u] + at.second) =
+                make_uint2(bf16x2_of(x[4], x[5]), bf16x2_of(x[6], x[7]));
+        }
     }
 }
 
