@@ -10,9 +10,12 @@
 // count position * inv_freq / 2pi is formed and reduced in fp64; cosine and
 // sine of the remaining half turn are fp32.
 //
-// Bound by memory traffic: 2 bytes in and 2 out an element.  There is no
-// cosine table to read: a block computes the pairs of its few tokens once
-// into shared memory and all heads of those tokens use them.
+// Bound by memory traffic, 2 bytes in and 2 out an element, and nearly by
+// instructions: about 56 for a lane's eight elements.  A warp keeps one token,
+// so that its lanes' cosines and sines stay in registers for all heads of q and
+// k (there is no table to read), as do the weights; pairs of values are
+// multiplied and added at once.  Several warps share a token where there are
+// few of them.
 #include <cuda_runtime.h>
 
 #include "fp4_device.cuh"
@@ -21,8 +24,8 @@ namespace fp8q {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxTokens = 4;      // tokens of a block
+constexpr int kThreads = 128;
+constexpr int kUnroll = 2;         // heads of a lane under way
 
 // A lane's eight elements of a head as two runs of four: `first` and
 // `second` start elements, and the first rotary pair they belong to (-1:
@@ -38,117 +41,178 @@ __device__ __forceinline__ LanePlace lane_place(int32_t lane, int32_t rotary) {
     return {4 * lane, rotary / 2 + 4 * lane, 4 * lane};
 }
 
+// Two fp32 values in one 64-bit register.
+struct Two {
+    uint64_t v;
+    __device__ __forceinline__ Two() {}
+    __device__ __forceinline__ Two(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y)); }
+    __device__ __forceinline__ float x() const { return __uint_as_float(static_cast<uint32_t>(v)); }
+    __device__ __forceinline__ float y() const { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+};
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+    Two d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+    Two d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return d;
+}
+__device__ __forceinline__ Two two_of(uint32_t bf16_pair) { return Two(bf16_low(bf16_pair), bf16_high(bf16_pair)); }
+__device__ __forceinline__ uint32_t bf16_of(Two a) { return bf16x2_of(a.x(), a.y()); }
+
+// What turns a lane's eight elements: for the half layout cosines, minus sines
+// and sines of pairs 0, 1 and 2, 3; interleaved the same of one pair each.
+template <bool kInterleaved>
+struct Turn {
+    Two c[kInterleaved ? 4 : 2], s[kInterleaved ? 4 : 2], minus_s[kInterleaved ? 1 : 2];
+};
+
 template <int D, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const QkNormRope p,
-                                                                int32_t tokens_per_block,
-                                                                int32_t parts) {
+__global__ void __launch_bounds__(kThreads, 8) qk_norm_rope_kernel(const QkNormRope p, int32_t parts) {
     constexpr int kLanes = D / 8;               // lanes of one head
-    constexpr int kGroups = kThreads / kLanes;  // heads in flight in the block
-    __shared__ float2 turns[kMaxTokens][D / 2];
+    constexpr int kCopies = 32 / kLanes;        // heads of a warp's pass
     pdl_wait();
     pdl_allow_next();
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x / parts) * tokens_per_block;
-    const int32_t part = blockIdx.x % parts;
-    const int32_t tokens = static_cast<int32_t>(
-        p.num_tokens - t0 < tokens_per_block ? p.num_tokens - t0 : tokens_per_block);
-    const int32_t half = p.rotary / 2;
-    for (int32_t i = threadIdx.x; i < tokens * half; i += kThreads) {
-        const int32_t t = i / half, j = i - t * half;
-        double u = static_cast<double>(p.positions[t0 + t]) * p.inv_freq[j] *
-                   0.15915494309189533577;   // turns: angle / 2pi
-        u -= rint(u);
-        float sn, cs;
-        sincospif(2.0f * static_cast<float>(u), &sn, &cs);
-        turns[t][j] = make_float2(cs * p.rope_scale, sn * p.rope_scale);
-    }
-    __syncthreads();
+    const uint32_t warp = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+    const int32_t lane = threadIdx.x % 32, copy = lane / kLanes;
+    const uint32_t part = warp % static_cast<uint32_t>(parts);
+    const int64_t token = warp / static_cast<uint32_t>(parts);
+    if (token >= p.num_tokens) return;          // the whole warp
+    const LanePlace at = lane_place<kInterleaved>(lane % kLanes, p.rotary);
 
-    const int32_t lane = threadIdx.x % kLanes;
-    const LanePlace at = lane_place<kInterleaved>(lane, p.rotary);
-    const int32_t heads = p.q_heads + p.k_heads;
-    const int32_t items = tokens * heads;
-    // Every thread of a warp runs the same number of passes, for the shuffles;
-    // a pass is kUnroll heads, all fetched before the first is used.
-    constexpr int kUnroll = 4;
-    const int32_t step = kGroups * parts;
-    for (int32_t base = part * kGroups; base < items; base += kUnroll * step) {
-        uint2 first[kUnroll], second[kUnroll];
-        uint16_t *dst[kUnroll];
-        int32_t token[kUnroll];                 // in the block; -1: no item
-        bool is_q[kUnroll];
+    // A batch of heads, `step` apart; the first of q is under way while the
+    // angles are made.
+    const int32_t step = parts * kCopies, mine = static_cast<int32_t>(part) * kCopies + copy;
+    uint2 lo[kUnroll], hi[kUnroll];
+    auto fetch = [&](const uint16_t *src, int32_t first, int32_t heads) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int32_t item = base + u * step + threadIdx.x / kLanes;
-            first[u] = second[u] = make_uint2(0, 0);
-            token[u] = -1;
-            if (item < items) {
-                const int32_t t = tokens == 1 ? 0 : item / heads, h = item - t * heads;
-                is_q[u] = h < p.q_heads;
-                const int64_t row = t0 + t;
-                const int32_t head = is_q[u] ? h : h - p.q_heads;
-                const uint16_t *src =
-                    (is_q[u] ? p.q + row * p.q_stride : p.k + row * p.k_stride) + head * D;
-                dst[u] = (is_q[u] ? p.q_out + row * p.q_out_stride : p.k_out + row * p.k_out_stride) + head * D;
-                token[u] = t;
-                first[u] = *reinterpret_cast<const uint2 *>(src + at.first);
-                second[u] = *reinterpret_cast<const uint2 *>(src + at.second);
+            const int32_t h = first + u * step;
+            lo[u] = hi[u] = make_uint2(0, 0);
+            if (h < heads) {
+                lo[u] = *reinterpret_cast<const uint2 *>(src + h * D + at.first);
+                hi[u] = *reinterpret_cast<const uint2 *>(src + h * D + at.second);
             }
         }
+    };
+    const uint16_t *q = p.q + token * p.q_stride, *k = p.k + token * p.k_stride;
+    const double position = static_cast<double>(p.positions[token]);
+    fetch(q, mine, p.q_heads);
+
+    // Cosines and sines of the token's pairs, shared out over the lanes.
+    Turn<kInterleaved> turn;
+    {
+        __shared__ alignas(16) float2 turns[kThreads / 32][D / 2];
+        float2 (&mine_turns)[D / 2] = turns[threadIdx.x / 32];
+        for (int32_t j = lane; j < p.rotary / 2; j += 32) {
+            double u = position * p.inv_freq[j] * 0.15915494309189533577;   // turns: angle / 2pi
+            u -= rint(u);
+            float sn, cs;
+            sincospif(2.0f * static_cast<float>(u), &sn, &cs);
+            mine_turns[j] = make_float2(cs * p.rope_scale, sn * p.rope_scale);
+        }
+        __syncwarp();
+        float cs[4], sn[4];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const uint2 a = first[u], b = second[u];
-            float x[8] = {bf16_low(a.x), bf16_high(a.x), bf16_low(a.y), bf16_high(a.y),
-                          bf16_low(b.x), bf16_high(b.x), bf16_low(b.y), bf16_high(b.y)};
-            float sum = 0.0f;
+        for (int i = 0; i < 4; ++i) cs[i] = sn[i] = 0.0f;
+        if (at.pair >= 0) {
+            const float4 a = reinterpret_cast<const float4 *>(mine_turns)[at.pair / 2];
+            const float4 b = reinterpret_cast<const float4 *>(mine_turns)[at.pair / 2 + 1];
+            cs[0] = a.x, sn[0] = a.y, cs[1] = a.z, sn[1] = a.w;
+            cs[2] = b.x, sn[2] = b.y, cs[3] = b.z, sn[3] = b.w;
+        }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-            if (token[u] < 0) continue;
-            const uint16_t *weight = is_q[u] ? p.q_weight : p.k_weight;
-            if (weight != nullptr) {
-                const float n = rsqrtf(sum * (1.0f / D) + p.eps);
-                const uint2 wa = *reinterpret_cast<const uint2 *>(weight + at.first);
-                const uint2 wb = *reinterpret_cast<const uint2 *>(weight + at.second);
-                const float w[8] = {bf16_low(wa.x), bf16_high(wa.x), bf16_low(wa.y), bf16_high(wa.y),
-                                    bf16_low(wb.x), bf16_high(wb.x), bf16_low(wb.y), bf16_high(wb.y)};
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = x[i] * n * w[i];
+        for (int i = 0; i < (kInterleaved ? 4 : 2); ++i) {
+            if (kInterleaved) {
+                turn.c[i] = Two(cs[i], cs[i]);
+                turn.s[i] = Two(-sn[i], sn[i]);
+            } else {
+                turn.c[i] = Two(cs[2 * i], cs[2 * i + 1]);
+                turn.s[i] = Two(sn[2 * i], sn[2 * i + 1]);
+                turn.minus_s[i] = Two(-sn[2 * i], -sn[2 * i + 1]);
             }
-            if (at.pair >= 0) {
+        }
+    }
+
+    auto heads_of = [&](const uint16_t *src, uint16_t *dst, int32_t heads, const uint16_t *weight) {
+        Two w[4];
+        if (weight != nullptr) {
+            const uint2 a = *reinterpret_cast<const uint2 *>(weight + at.first);
+            const uint2 b = *reinterpret_cast<const uint2 *>(weight + at.second);
+            w[0] = two_of(a.x), w[1] = two_of(a.y), w[2] = two_of(b.x), w[3] = two_of(b.y);
+        }
+        // Every lane runs the same passes, for the shuffles.
+        for (int32_t first = mine; first - copy < heads;) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 cs = turns[token[u]][at.pair + i];
-                    const int s = kInterleaved ? 2 * i : i, v = kInterleaved ? 2 * i + 1 : i + 4;
-                    const float c = x[s], e = x[v];
-                    x[s] = c * cs.x - e * cs.y;
-                    x[v] = e * cs.x + c * cs.y;
+            for (int u = 0; u < kUnroll; ++u) {
+                const int32_t h = first + u * step;
+                Two x[4] = {two_of(lo[u].x), two_of(lo[u].y), two_of(hi[u].x), two_of(hi[u].y)};
+                if (weight != nullptr) {
+                    Two sums = mul2(x[0], x[0]);
+#pragma unroll
+                    for (int i = 1; i < 4; ++i) sums = fma2(x[i], x[i], sums);
+                    float sum = sums.x() + sums.y();
+#pragma unroll
+                    for (int o = kLanes / 2; o > 0; o /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+                    const float n = rsqrtf(sum * (1.0f / D) + p.eps);
+                    const Two nn(n, n);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = mul2(mul2(x[i], nn), w[i]);
+                }
+                if (at.pair >= 0) {
+                    if (kInterleaved) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            x[i] = fma2(Two(x[i].y(), x[i].x()), turn.s[i], mul2(x[i], turn.c[i]));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const Two a = x[i], b = x[2 + i];
+                            x[i] = fma2(b, turn.minus_s[i], mul2(a, turn.c[i]));
+                            x[2 + i] = fma2(a, turn.s[i], mul2(b, turn.c[i]));
+                        }
+                    }
+                }
+                if (h < heads) {
+                    *reinterpret_cast<uint2 *>(dst + h * D + at.first) = make_uint2(bf16_of(x[0]), bf16_of(x[1]));
+                    *reinterpret_cast<uint2 *>(dst + h * D + at.second) = make_uint2(bf16_of(x[2]), bf16_of(x[3]));
                 }
             }
-            *reinterpret_cast<uint2 *>(dst[u] + at.first) =
-                make_uint2(bf16x2_of(x[0], x[1]), bf16x2_of(x[2], x[3]));
-            *reinterpret_cast<uint2 *>(dst[u] + at.second) =
-                make_uint2(bf16x2_of(x[4], x[5]), bf16x2_of(x[6], x[7]));
+            first += kUnroll * step;
+            if (first - copy < heads) fetch(src, first, heads);
         }
-    }
+    };
+    heads_of(q, p.q_out + token * p.q_out_stride, p.q_heads, p.q_weight);
+    fetch(k, mine, p.k_heads);
+    heads_of(k, p.k_out + token * p.k_out_stride, p.k_heads, p.k_weight);
 }
 
 template <int D>
-cudaError_t launch_dim(const QkNormRope &r, cudaStream_t stream) {
-    constexpr int kGroups = kThreads / (D / 8);
+cudaError_t launch_dim(QkNormRope r, cudaStream_t stream) {
+    constexpr int kCopies = 256 / D;
     auto kernel = r.interleaved ? qk_norm_rope_kernel<D, true> : qk_norm_rope_kernel<D, false>;
-    const int64_t heads = static_cast<int64_t>(r.q_heads) + r.k_heads;
-    // Enough blocks to fill the GPU: fewer tokens a block first, then the
-    // heads of a token split over several blocks.
-    constexpr int64_t kFull = 148 * 8;
-    int64_t per_block = r.num_tokens / kFull;
-    per_block = per_block < 1 ? 1 : per_block > kMaxTokens ? kMaxTokens : per_block;
-    const int64_t groups = (r.num_tokens + per_block - 1) / per_block;
-    int64_t parts = kFull / groups;
-    const int64_t most = (per_block * heads + kGroups - 1) / kGroups;
+    // Warps of a token: as many as fill the GPU, up to one pass of a head each.
+    constexpr int64_t kFull = 148 * 32;
+    const int64_t most = ((r.q_heads > r.k_heads ? r.q_heads : r.k_heads) + kCopies - 1) / kCopies;
+    int64_t parts = kFull / r.num_tokens;
     parts = parts < 1 ? 1 : parts > most ? most : parts;
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(groups * parts)), kThreads, 0, stream, r,
-                      static_cast<int32_t>(per_block), static_cast<int32_t>(parts));
+    // Warp indexes are 32 bits inside a launch.
+    const int64_t chunk = (int64_t{1} << 30) / parts;
+    for (int64_t left = r.num_tokens; left > 0; left -= chunk) {
+        r.num_tokens = left < chunk ? left : chunk;
+        const int64_t blocks = (r.num_tokens * parts + kThreads / 32 - 1) / (kThreads / 32);
+        const cudaError_t e = launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), kThreads, 0, stream, r,
+                                         static_cast<int32_t>(parts));
+        if (e != cudaSuccess) return e;
+        r.positions += chunk;
+        r.q += chunk * r.q_stride;
+        r.k += chunk * r.k_stride;
+        r.q_out += chunk * r.q_out_stride;
+        r.k_out += chunk * r.k_out_stride;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace
