@@ -10,7 +10,9 @@ ABI.  Importing fails if the library has not been built.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -393,6 +395,15 @@ def load_scales(path: str) -> list[tuple[float, float]]:
 # the 4-bit paged KV cache
 
 
+try:                       # what the public functions wrap, at a tenth of the time
+    from torch._C import _cuda_getCurrentRawStream as _current_raw_stream
+    from torch._C import _cuda_getDevice as _current_device
+except ImportError:
+    def _current_raw_stream(device):
+        return torch.cuda.current_stream(device).cuda_stream
+    _current_device = torch.cuda.current_device
+
+
 def _rows3(t: torch.Tensor, name: str) -> int:
     """Row stride in elements of a CUDA bf16 ``[T, heads, dim]`` tensor whose
     rows are contiguous."""
@@ -406,20 +417,20 @@ def _rows3(t: torch.Tensor, name: str) -> int:
     return s0 if n > 1 else heads * dim
 
 
-def _same_device(device: int, **tensors) -> None:
-    for name, t in tensors.items():
+def _same_device(device: int, names: tuple, tensors: tuple) -> None:
+    for i, t in enumerate(tensors):
         if t is not None and t.get_device() != device:
-            raise ValueError(f"{name} must be on the same CUDA device as the other tensors")
+            raise ValueError(f"{names[i]} must be on the same CUDA device as the other tensors")
 
 
 def _call_on(device: int, stream, name: str, fn, *args) -> None:
     """Call the library with ``device`` current; no stream given means the
     current stream of that device."""
     if stream is None:
-        raw = torch.cuda.current_stream(device).cuda_stream
+        raw = _current_raw_stream(device)
     else:
         raw = stream if isinstance(stream, int) else stream.cuda_stream
-    if torch.cuda.current_device() == device:
+    if _current_device() == device:
         status = fn(*args, raw)
     else:
         with torch.cuda.device(device):
@@ -478,8 +489,8 @@ def _fp4_rows(k: torch.Tensor, v: torch.Tensor, slot_mapping, k_pool, v_pool, sc
     if (heads, dim) != (pool_heads, pool_dim):
         raise ValueError(f"pools hold {pool_heads} heads of {pool_dim}, k and v have {heads} of {dim}")
     device = k.get_device()
-    _same_device(device, v=v, k_pool=k_pool, v_pool=v_pool, scale_dev=scale_dev,
-                 slot_mapping=slot_mapping if t else None)
+    _same_device(device, ("v", "k_pool", "v_pool", "scale_dev", "slot_mapping"),
+                 (v, k_pool, v_pool, scale_dev, slot_mapping if t else None))
     return device, (k.data_ptr(), v.data_ptr(), ks, vs, slot_mapping.data_ptr(), t, heads, dim,
                     k_pool.data_ptr(), v_pool.data_ptr(), bs, stride, nb)
 
@@ -515,11 +526,14 @@ def fp4_kv_read(slot_mapping: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.
     return k_out, v_out
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _allocating_for(stream, device: torch.device):
     """Context in which tensors belong to ``stream``, so that their memory is
     not handed out again before the stream's work on them is done."""
     if stream is None:
-        return torch.cuda.device(device)
+        return _HERE if device.index == _current_device() else torch.cuda.device(device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device)
     return torch.cuda.stream(stream)
@@ -530,6 +544,7 @@ def _check_index(t: torch.Tensor, name: str, *shape) -> None:
         raise ValueError(f"{name} must be int32 {list(shape)}")
 
 
+@functools.lru_cache(maxsize=256)
 def fp4_kv_attention_workspace(batch: int, num_tokens: int, num_q_heads: int, num_kv_heads: int,
                                head_dim: int) -> int:
     """Bytes of workspace fp4_kv_attention needs for these sizes."""
@@ -598,8 +613,9 @@ def fp4_kv_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor
         raise ValueError("lse must be a contiguous float32 tensor [T, q_heads]")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    _same_device(device, k_pool=k_pool, v_pool=v_pool, block_table=block_table, seq_lens=seq_lens,
-                 q_start=q_start, scale_dev=scale_dev, out=out, lse=lse, workspace=workspace)
+    _same_device(device, ("k_pool", "v_pool", "block_table", "seq_lens", "q_start", "scale_dev", "out",
+                          "lse", "workspace"),
+                 (k_pool, v_pool, block_table, seq_lens, q_start, scale_dev, out, lse, workspace))
     _call_on(device, stream, "fp4_kv_attention", lib.fp4_kv_attention,
              q.data_ptr(), q_stride, k_pool.data_ptr(), v_pool.data_ptr(), bs, stride, nb, heads,
              dim, block_table.data_ptr(), table_stride, width, seq_lens.data_ptr(), _ptr(q_start),
@@ -682,8 +698,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor,
     if q_out.shape != q.shape or k_out.shape != k.shape:
         raise ValueError("q_out and k_out must have the shapes of q and k")
     qo_stride, ko_stride = _rows3(q_out, "q_out"), _rows3(k_out, "k_out")
-    _same_device(device, k=k, positions=positions, inv_freq=inv_freq, q_weight=q_weight,
-                 k_weight=k_weight, q_out=q_out, k_out=k_out)
+    _same_device(device, ("k", "positions", "inv_freq", "q_weight", "k_weight", "q_out", "k_out"),
+                 (k, positions, inv_freq, q_weight, k_weight, q_out, k_out))
     _call_on(device, stream, "qk_norm_rope", lib.qk_norm_rope,
              q.data_ptr(), k.data_ptr(), q_stride, k_stride, q_out.data_ptr(), k_out.data_ptr(),
              qo_stride, ko_stride, positions.data_ptr(), inv_freq.data_ptr(), _ptr(q_weight),

@@ -35,8 +35,7 @@
 // while this one's sums are finished.  It is the copies that have to be few:
 // of 1152 bytes each (16 tokens of one head of 128) the copying warps kept
 // 4.1 TB/s whether or not anything was computed.  So a block takes four, two or one
-// heads at once, whatever divides their number, with one, two or four of its
-// warps on each: the heads of a page lie side by side, and one copy takes all
+// heads at once, with one, two or four of its warps on each: the heads of a page lie side by side, and one copy takes all
 // of them when a page is 16 tokens, or 32 tokens of one when it is longer.
 // The running maximum is joined over lanes only when some lane sees a larger
 // score.
@@ -1006,8 +1005,30 @@ int tiles_of(int64_t batch, int64_t num_tokens, int32_t group, int32_t dim) {
     return rows <= 8 || dim == 256 ? 1 : 2;
 }
 
-// Warps of a head: a block takes as many of four heads as divide their number.
-int warps_of_head(int32_t kv_heads) { return kv_heads % 4 == 0 ? 1 : kv_heads % 2 == 0 ? 2 : 4; }
+// Sets of four heads with their row tiles, at least: below 32 no block takes
+// four heads at once, whatever the lengths.
+int64_t fours_of(int64_t batch, int64_t num_tokens, int32_t group, int32_t kv_heads, int32_t rows) {
+    if (kv_heads % 4 != 0) return 0;
+    const int64_t tiles = (num_tokens * group + rows - 1) / rows;
+    return (tiles > batch ? tiles : batch) * (kv_heads / 4);
+}
+constexpr int64_t kFewFours = 32;
+
+// Warps of a head: a block takes as many of two heads as divide their number,
+// and four where the blocks' runs can be long.  Four heads in one copy read
+// faster, and leave twice the parts to join.  Measured with 4 heads of 128 and
+// 3000-6000 tokens, four heads against two: 48 sequences (20 steps of a block)
+// 38.9 and 38.2 us, 96 (41) 61.2 and 61.5, 160 (68) 88.9 and 93.2; 64 of 1-8192
+// (37 if all were as long as the longest) 30.0 and 26.9; with rows for two
+// tiles, 32 drafts (37) 36.7 and 39.5.
+int warps_of_head(const Fp4Attention &a, int32_t rows) {
+    const int32_t heads = a.pools.heads;
+    const int64_t fours = fours_of(a.batch, a.num_tokens, a.q_heads / heads, heads, rows);
+    const int64_t blocks = kMaxBlocks / 3 * (rows * a.pools.dim <= 1024 ? 3 : 2);
+    const int64_t steps = a.table_width * a.pools.tiles / 2;
+    if (fours >= kFewFours && fours * steps >= (rows == 8 ? 40 : 32) * blocks) return 1;
+    return heads % 2 == 0 ? 2 : 4;
+}
 
 template <int D, int NT, int T>
 cudaError_t launch_tiles(const Fp4Attention &a, cudaStream_t stream) {
@@ -1015,9 +1036,8 @@ cudaError_t launch_tiles(const Fp4Attention &a, cudaStream_t stream) {
     constexpr size_t kSmem = sizeof(Shared<D, NT, T>);
     static_assert(S::kBlocks * (kSmem + 1024) <= 228 * 1024, "the blocks of an SM fit its shared memory");
     auto kernel = fp4_attention_kernel<D, NT, T>;
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    int sms = 0;
+    cudaError_t e = device_sms(&sms);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(kSmem));
@@ -1057,7 +1077,7 @@ cudaError_t launch_tiles(const Fp4Attention &a, cudaStream_t stream) {
 
 template <int D, int NT>
 cudaError_t launch_heads(const Fp4Attention &a, cudaStream_t stream) {
-    const int t = warps_of_head(a.pools.heads);
+    const int t = warps_of_head(a, 8 * NT);
     return t == 1 ? launch_tiles<D, NT, 1>(a, stream)
            : t == 2 ? launch_tiles<D, NT, 2>(a, stream) : launch_tiles<D, NT, 4>(a, stream);
 }
@@ -1076,10 +1096,12 @@ bool fp4_attention_by_rows(int64_t batch, int64_t num_tokens, int32_t group) {
 int64_t fp4_attention_workspace(int64_t batch, int64_t num_tokens, int32_t q_heads,
                                 int32_t kv_heads, int32_t dim) {
     if (batch == 0) return 0;
-    if (fp4_attention_by_rows(batch, num_tokens, q_heads / kv_heads)) return fp4_attention_rows_workspace(dim);
+    if (fp4_attention_by_rows(batch, num_tokens, q_heads / kv_heads)) return fp4_attention_rows_workspace(num_tokens, q_heads / kv_heads, kv_heads, dim);
     const int rows = 8 * tiles_of(batch, num_tokens, q_heads / kv_heads, dim);
     const int64_t blocks = rows * dim <= 1024 ? kMaxBlocks : kMaxBlocks / 3 * 2;   // as Shape::kBlocks
-    return kRecordBytes + blocks * 2 * 4 * (kWarps / warps_of_head(kv_heads)) * part_floats(rows, dim);
+    const int heads = fours_of(batch, num_tokens, q_heads / kv_heads, kv_heads, rows) >= kFewFours ? 4
+                      : kv_heads % 2 == 0 ? 2 : 1;     // of a block, at most
+    return kRecordBytes + blocks * 2 * 4 * heads * part_floats(rows, dim);
 }
 
 cudaError_t launch_fp4_attention(const Fp4Attention &a, cudaStream_t stream) {

@@ -781,15 +781,21 @@ __global__ void __launch_bounds__(kRows) fp4_attention_rows_join_kernel(const Fp
         a.lse[static_cast<int64_t>(place.token) * a.q_heads + place.q_head] = row_lse(top, l, kShift);
 }
 
+// Enough items to fill the blocks: none is split, and the parts (64 KB each with
+// 128 dimensions) and their join are saved.
+bool items_whole(int64_t num_tokens, int32_t group, int32_t kv_heads, int32_t dim) {
+    const int64_t tiles = (num_tokens * group + kRows - 1) / kRows;
+    return 2 * tiles * kv_heads >= 3 * (kMaxBlocks / 3) * (dim == 256 ? 1 : 2);
+}
+
 template <int D>
 cudaError_t launch_dim(const Fp4Attention &a, cudaStream_t stream) {
     using L = Layout<D>;
     constexpr size_t kSmem = sizeof(Shared<D>) + 1024;
     static_assert(L::kBlocks * (kSmem + 1024) <= 228 * 1024, "the blocks of an SM fit its shared memory");
     auto kernel = fp4_attention_rows_kernel<D>;
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    int sms = 0;
+    cudaError_t e = device_sms(&sms);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
     if (e != cudaSuccess) return e;
@@ -801,9 +807,7 @@ cudaError_t launch_dim(const Fp4Attention &a, cudaStream_t stream) {
     const int64_t items = (tiles + a.batch) * a.pools.heads;
     const int64_t longest = a.table_width * a.pools.tiles * 16 / kTokens + 2 + kItemCost;
     if (items < grid && items * longest < grid) grid = items * longest;
-    // Enough items to fill the blocks: none is split, and the parts (64 KB each
-    // with 128 dimensions) and their join are saved.
-    const bool whole = tiles * a.pools.heads >= grid + grid / 2;
+    const bool whole = items_whole(a.num_tokens, group, a.pools.heads, D);
     // Started on a free GPU, like the kernel for few rows.
     kernel<<<static_cast<unsigned>(grid), kThreads, kSmem, stream>>>(a, whole);
     e = cudaGetLastError();
@@ -815,8 +819,12 @@ cudaError_t launch_dim(const Fp4Attention &a, cudaStream_t stream) {
 
 }  // namespace
 
-int64_t fp4_attention_rows_workspace(int32_t dim) {
-    return kRecordBytes + static_cast<int64_t>(kMaxBlocks / 3) * (dim == 256 ? 1 : 2) * 2 * 4 * part_floats(kRows, dim);
+int64_t fp4_attention_rows_workspace(int64_t num_tokens, int32_t group, int32_t kv_heads,
+                                     int32_t dim) {
+    if (items_whole(num_tokens, group, kv_heads, dim)) return kRecordBytes;
+    // a block begins one item that goes on, and ends one
+    const int64_t blocks = kMaxBlocks / 3 * (dim == 256 ? 1 : 2);
+    return kRecordBytes + blocks * 2 * 4 * part_floats(kRows, dim);
 }
 
 cudaError_t launch_fp4_attention_rows(const Fp4Attention &a, cudaStream_t stream) {

@@ -41,6 +41,19 @@ cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, int block, size_t s
     return e;
 }
 
+// Multiprocessors of the current device.
+inline cudaError_t device_sms(int *sms) {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    *sms = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (*sms > 0) return cudaSuccess;
+    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess && dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
+    return e;
+}
+
 // Every kernel passes its dependency wait before it lets its dependents
 // start, so everything enqueued before it has completed when they start.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

@@ -69,7 +69,8 @@ cudaError_t launch_fp4_attention(const Fp4Attention &a, cudaStream_t stream);
 
 // Its kernel for many rows to a KV head (fp4_attention_rows.cu).
 bool fp4_attention_by_rows(int64_t batch, int64_t num_tokens, int32_t group);
-int64_t fp4_attention_rows_workspace(int32_t dim);
+int64_t fp4_attention_rows_workspace(int64_t num_tokens, int32_t group, int32_t kv_heads,
+                                     int32_t dim);
 cudaError_t launch_fp4_attention_rows(const Fp4Attention &a, cudaStream_t stream);
 
 struct QkNormRope {
