@@ -665,7 +665,9 @@ FP8Q_API fp8q_status fp4_kv_read(void *k, void *v, int64_t key_stride, int64_t v
  *   lse           device fp32 [num_tokens, num_q_heads], or NULL
  *   workspace     device memory of at least fp4_kv_attention_workspace(...)
  *                 bytes, 16-byte aligned.  It holds nothing between calls; two
- *                 calls that may run at the same time need one each.
+ *                 calls that may run at the same time need one each.  With
+ *                 fp4_kv_attention_workspace_uneven(...) bytes a sequence that
+ *                 is much longer than the others is shared out in every case.
  * Returns FP8Q_OK, FP8Q_EINVAL, FP8Q_ECUDA.
  */
 FP8Q_API fp8q_status fp4_kv_attention(const void *q, int64_t q_stride, const void *k_pool,
@@ -680,11 +682,15 @@ FP8Q_API fp8q_status fp4_kv_attention(const void *q, int64_t q_stride, const voi
                                       void *out, int64_t out_stride, float *lse, void *workspace,
                                       int64_t workspace_bytes, void *stream);
 
-/* Bytes of workspace fp4_kv_attention needs for these sizes; -1 for sizes it
+/* Bytes of workspace fp4_kv_attention needs for these sizes, and what it can
+ * use (the same or more) where sequences differ much in length; -1 for sizes it
  * refuses. */
 FP8Q_API int64_t fp4_kv_attention_workspace(int64_t batch, int64_t num_tokens,
                                             int32_t num_q_heads, int32_t num_kv_heads,
                                             int32_t head_dim);
+FP8Q_API int64_t fp4_kv_attention_workspace_uneven(int64_t batch, int64_t num_tokens,
+                                                   int32_t num_q_heads, int32_t num_kv_heads,
+                                                   int32_t head_dim);
 
 /* ------------------------------------------------------------------------ */
 /* 5. Norms of queries and keys with the position rotation                  */

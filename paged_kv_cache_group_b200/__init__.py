@@ -546,9 +546,11 @@ def _check_index(t: torch.Tensor, name: str, *shape) -> None:
 
 @functools.lru_cache(maxsize=256)
 def fp4_kv_attention_workspace(batch: int, num_tokens: int, num_q_heads: int, num_kv_heads: int,
-                               head_dim: int) -> int:
-    """Bytes of workspace fp4_kv_attention needs for these sizes."""
-    n = lib.fp4_kv_attention_workspace(batch, num_tokens, num_q_heads, num_kv_heads, head_dim)
+                               head_dim: int, uneven: bool = False) -> int:
+    """Bytes of workspace fp4_kv_attention needs for these sizes; with
+    ``uneven`` what it can use where sequences differ much in length."""
+    f = lib.fp4_kv_attention_workspace_uneven if uneven else lib.fp4_kv_attention_workspace
+    n = f(batch, num_tokens, num_q_heads, num_kv_heads, head_dim)
     if n < 0:
         raise ValueError("sizes fp4_kv_attention does not take")
     return n
@@ -572,7 +574,7 @@ def fp4_kv_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor
     to dim ** -0.5.  Returns ``out``, or ``(out, lse)`` when an fp32 ``lse
     [T, q_heads]`` is given to be filled.  ``workspace`` (uint8, at least
     fp4_kv_attention_workspace() bytes) is allocated for the call when not
-    given; calls that may overlap need one each."""
+    given, for sequences of any lengths; calls that may overlap need one each."""
     if q.dim() != 3:
         raise ValueError("q must be [T, heads, dim]")
     q_stride = _rows3(q, "q")
@@ -603,7 +605,7 @@ def fp4_kv_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor
             if out is None:
                 out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
             if workspace is None:
-                workspace = torch.empty(fp4_kv_attention_workspace(batch, t, q_heads, heads, dim),
+                workspace = torch.empty(fp4_kv_attention_workspace(batch, t, q_heads, heads, dim, True),
                                         dtype=torch.uint8, device=q.device)
     if out.shape != q.shape:
         raise ValueError("out must have the shape of q")

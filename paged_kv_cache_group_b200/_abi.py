@@ -81,6 +81,7 @@ SIGNATURES = {
                                   _P, _P, _I64, _I64, _I32, _F, _I64, _F, _F, _P, _P, _I64, _P,
                                   _P, _I64, _P]),
     "fp4_kv_attention_workspace": (_I64, [_I64, _I64, _I32, _I32, _I32]),
+    "fp4_kv_attention_workspace_uneven": (_I64, [_I64, _I64, _I32, _I32, _I32]),
     "qk_norm_rope": (STATUS, [_P, _P, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _P, _P, _I64, _I32,
                               _I32, _I32, _I32, _I32, _F, _F, _P]),
     "fp8q_device_error": (STATUS, [c.POINTER(c.c_uint32), _I32]),

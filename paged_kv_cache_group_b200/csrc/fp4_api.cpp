@@ -124,7 +124,14 @@ FP8Q_API int64_t fp4_kv_attention_workspace(int64_t batch, int64_t num_tokens,
                                             int32_t num_q_heads, int32_t num_kv_heads,
                                             int32_t head_dim) {
     if (!valid_attention_sizes(batch, num_tokens, num_q_heads, num_kv_heads, head_dim)) return -1;
-    return fp8q::fp4_attention_workspace(batch, num_tokens, num_q_heads, num_kv_heads, head_dim);
+    return fp8q::fp4_attention_workspace(batch, num_tokens, num_q_heads, num_kv_heads, head_dim, false);
+}
+
+FP8Q_API int64_t fp4_kv_attention_workspace_uneven(int64_t batch, int64_t num_tokens,
+                                                   int32_t num_q_heads, int32_t num_kv_heads,
+                                                   int32_t head_dim) {
+    if (!valid_attention_sizes(batch, num_tokens, num_q_heads, num_kv_heads, head_dim)) return -1;
+    return fp8q::fp4_attention_workspace(batch, num_tokens, num_q_heads, num_kv_heads, head_dim, true);
 }
 
 FP8Q_API fp8q_status fp4_kv_attention(const void *q, int64_t q_stride, const void *k_pool,
@@ -160,7 +167,7 @@ FP8Q_API fp8q_status fp4_kv_attention(const void *q, int64_t q_stride, const voi
     if ((table_width > 0 && block_table == nullptr) || !aligned(block_table, 4)) return FP8Q_EINVAL;
     if (workspace == nullptr || !aligned(workspace, 16) ||
         workspace_bytes < fp8q::fp4_attention_workspace(batch, num_tokens, num_q_heads,
-                                                        num_kv_heads, head_dim))
+                                                        num_kv_heads, head_dim, false))
         return FP8Q_EINVAL;
     a.q = static_cast<const uint16_t *>(q);
     a.q_stride = q_stride;
@@ -178,6 +185,7 @@ FP8Q_API fp8q_status fp4_kv_attention(const void *q, int64_t q_stride, const voi
     a.window = window > kMaxRows ? 0 : static_cast<int32_t>(window);   // wider than any table
     a.softmax_scale = softmax_scale;
     a.workspace = workspace;
+    a.workspace_bytes = workspace_bytes;
     return from_cuda(fp8q::launch_fp4_attention(a, static_cast<cudaStream_t>(stream)));
 }
 

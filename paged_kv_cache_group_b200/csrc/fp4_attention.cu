@@ -1094,9 +1094,9 @@ bool fp4_attention_by_rows(int64_t batch, int64_t num_tokens, int32_t group) {
 }
 
 int64_t fp4_attention_workspace(int64_t batch, int64_t num_tokens, int32_t q_heads,
-                                int32_t kv_heads, int32_t dim) {
+                                int32_t kv_heads, int32_t dim, bool uneven) {
     if (batch == 0) return 0;
-    if (fp4_attention_by_rows(batch, num_tokens, q_heads / kv_heads)) return fp4_attention_rows_workspace(num_tokens, q_heads / kv_heads, kv_heads, dim);
+    if (fp4_attention_by_rows(batch, num_tokens, q_heads / kv_heads)) return fp4_attention_rows_workspace(num_tokens, q_heads / kv_heads, kv_heads, dim, uneven);
     const int rows = 8 * tiles_of(batch, num_tokens, q_heads / kv_heads, dim);
     const int64_t blocks = rows * dim <= 1024 ? kMaxBlocks : kMaxBlocks / 3 * 2;   // as Shape::kBlocks
     const int heads = fours_of(batch, num_tokens, q_heads / kv_heads, kv_heads, rows) >= kFewFours ? 4

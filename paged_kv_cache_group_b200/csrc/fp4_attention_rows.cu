@@ -193,7 +193,8 @@ __device__ __forceinline__ void walk_items(const Fp4Attention &a, Control &c, co
         if (walk.start >= run.end) break;
         int32_t r0 = static_cast<int32_t>(max(int64_t{0}, run.at - unit0));
         int32_t r1 = static_cast<int32_t>(max(int64_t{0}, min(static_cast<int64_t>(x.units), run.end - unit0)));
-        if (d.whole) {                   // the block that has an item's middle takes all of it
+        if (d.whole == 1 || (d.whole == 2 && x.units + kItemCost <= run.per_block)) {
+            // the block that has an item's middle takes all of it
             const int64_t middle = walk.start + (x.units + kItemCost) / 2;
             r0 = 0;
             r1 = middle >= run.at && middle < run.end ? x.units : 0;
@@ -724,37 +725,41 @@ __global__ void __launch_bounds__(kThreads, Layout<D>::kBlocks) fp4_attention_ro
     }
 }
 
-// Block (c, y) merges 8 dimensions of the item that began in block c, a row a
+constexpr int kJoinDims = 16;          // of a thread
+
+// Block (c, y) merges 16 dimensions of the item that began in block c, a row a
 // thread.
 template <int D>
 __global__ void __launch_bounds__(kRows) fp4_attention_rows_join_kernel(const Fp4Attention a) {
     using L = Layout<D>;
-    constexpr int kBatch = 4;
+    constexpr int kBatch = 2, kQuads = kJoinDims / 4;
     pdl_wait();
     pdl_allow_next();
     const int32_t c = blockIdx.x, row = threadIdx.x;
     const Split s = static_cast<const Split *>(a.workspace)[c];
-    if (row / 32 * 32 >= s.rows || s.blocks == 0) return;
+    if (s.blocks == 0 || row >= s.rows) return;
     float k_scale, v_scale;
     load_scales(a, &k_scale, &v_scale);
-    float top = -INFINITY, l = 0.0f, x[8];
+    float top = -INFINITY, l = 0.0f, x[kJoinDims];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = 0.0f;
+    for (int j = 0; j < kJoinDims; ++j) x[j] = 0.0f;
     for (int32_t i0 = 0; i0 < s.blocks; i0 += kBatch) {
         float t[kBatch], m[kBatch];
-        float4 v[kBatch][2];
+        float4 v[kBatch][kQuads];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             const int32_t i = i0 + k;
             t[k] = -INFINITY, m[k] = 0.0f;
-            v[k][0] = v[k][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int j = 0; j < kQuads; ++j) v[k][j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (i < s.blocks) {
                 // part 1 of block c, then part 0 of the blocks behind it
                 const float *p = part_at(a.workspace, 2 * static_cast<int64_t>(c + i) + (i == 0 ? 1 : 0), L::kPartFloats);
                 t[k] = p[kRows * D + row];
                 m[k] = p[kRows * D + kRows + row];
-                v[k][0] = reinterpret_cast<const float4 *>(p)[(2 * blockIdx.y) * kRows + row];
-                v[k][1] = reinterpret_cast<const float4 *>(p)[(2 * blockIdx.y + 1) * kRows + row];
+#pragma unroll
+                for (int j = 0; j < kQuads; ++j)
+                    v[k][j] = reinterpret_cast<const float4 *>(p)[(kQuads * blockIdx.y + j) * kRows + row];
             }
         }
 #pragma unroll
@@ -764,25 +769,31 @@ __global__ void __launch_bounds__(kRows) fp4_attention_rows_join_kernel(const Fp
             const float f = exp2_fast(top - base), e = exp2_fast(t[k] - base);
             top = now;
             l = l * f + m[k] * e;
-            const float w[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w,
-                                v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = x[j] * f + w[j] * e;
+            for (int j = 0; j < kQuads; ++j) {
+                x[4 * j] = x[4 * j] * f + v[k][j].x * e;
+                x[4 * j + 1] = x[4 * j + 1] * f + v[k][j].y * e;
+                x[4 * j + 2] = x[4 * j + 2] * f + v[k][j].z * e;
+                x[4 * j + 3] = x[4 * j + 3] * f + v[k][j].w * e;
+            }
         }
     }
-    if (row >= s.rows) return;
     const RowPlace place = row_place(s.token0, s.row0 + row, s.set, a.q_heads / a.pools.heads);
     const float inv = row_factor(l, v_scale);
-    *reinterpret_cast<uint4 *>(a.out + place.token * a.out_stride + static_cast<int64_t>(place.q_head) * D +
-                               8 * blockIdx.y) =
-        make_uint4(bf16x2_of(x[0] * inv, x[1] * inv), bf16x2_of(x[2] * inv, x[3] * inv),
-                   bf16x2_of(x[4] * inv, x[5] * inv), bf16x2_of(x[6] * inv, x[7] * inv));
+    uint4 *out = reinterpret_cast<uint4 *>(a.out + place.token * a.out_stride +
+                                           static_cast<int64_t>(place.q_head) * D + kJoinDims * blockIdx.y);
+#pragma unroll
+    for (int j = 0; j < kJoinDims; j += 8)
+        out[j / 8] = make_uint4(bf16x2_of(x[j] * inv, x[j + 1] * inv), bf16x2_of(x[j + 2] * inv, x[j + 3] * inv),
+                                bf16x2_of(x[j + 4] * inv, x[j + 5] * inv), bf16x2_of(x[j + 6] * inv, x[j + 7] * inv));
     if (a.lse != nullptr && blockIdx.y == 0)
         a.lse[static_cast<int64_t>(place.token) * a.q_heads + place.q_head] = row_lse(top, l, kShift);
 }
 
-// Enough items to fill the blocks: none is split, and the parts (64 KB each with
-// 128 dimensions) and their join are saved.
+// Enough items to fill the blocks: they are not split, and the parts (64 KB each
+// with 128 dimensions) are saved; but where there is room for parts, items that
+// cost more than a block's share are, or one long sequence among short ones
+// would be left to a few blocks.
 bool items_whole(int64_t num_tokens, int32_t group, int32_t kv_heads, int32_t dim) {
     const int64_t tiles = (num_tokens * group + kRows - 1) / kRows;
     return 2 * tiles * kv_heads >= 3 * (kMaxBlocks / 3) * (dim == 256 ? 1 : 2);
@@ -807,21 +818,23 @@ cudaError_t launch_dim(const Fp4Attention &a, cudaStream_t stream) {
     const int64_t items = (tiles + a.batch) * a.pools.heads;
     const int64_t longest = a.table_width * a.pools.tiles * 16 / kTokens + 2 + kItemCost;
     if (items < grid && items * longest < grid) grid = items * longest;
-    const bool whole = items_whole(a.num_tokens, group, a.pools.heads, D);
+    int32_t whole = 0;
+    if (items_whole(a.num_tokens, group, a.pools.heads, D))
+        whole = a.workspace_bytes >= fp4_attention_rows_workspace(a.num_tokens, group, a.pools.heads, D, true) ? 2 : 1;
     // Started on a free GPU, like the kernel for few rows.
     kernel<<<static_cast<unsigned>(grid), kThreads, kSmem, stream>>>(a, whole);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     g_launch_count.fetch_add(1, std::memory_order_relaxed);
-    if (whole) return cudaSuccess;
-    return launch_pdl(fp4_attention_rows_join_kernel<D>, dim3(static_cast<unsigned>(grid), D / 8), kRows, 0, stream, a);
+    if (whole == 1) return cudaSuccess;
+    return launch_pdl(fp4_attention_rows_join_kernel<D>, dim3(static_cast<unsigned>(grid), D / kJoinDims), kRows, 0, stream, a);
 }
 
 }  // namespace
 
-int64_t fp4_attention_rows_workspace(int64_t num_tokens, int32_t group, int32_t kv_heads,
-                                     int32_t dim) {
-    if (items_whole(num_tokens, group, kv_heads, dim)) return kRecordBytes;
+int64_t fp4_attention_rows_workspace(int64_t num_tokens, int32_t group, int32_t kv_heads, int32_t dim,
+                                     bool uneven) {
+    if (items_whole(num_tokens, group, kv_heads, dim) && !uneven) return kRecordBytes;
     // a block begins one item that goes on, and ends one
     const int64_t blocks = kMaxBlocks / 3 * (dim == 256 ? 1 : 2);
     return kRecordBytes + blocks * 2 * 4 * part_floats(kRows, dim);

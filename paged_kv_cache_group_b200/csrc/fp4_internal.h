@@ -60,17 +60,19 @@ struct Fp4Attention {
     int32_t window = 0;                 // 0: no window
     float softmax_scale = 1.0f;
     void *workspace = nullptr;
+    int64_t workspace_bytes = 0;
 };
 
-// Bytes of workspace launch_fp4_attention uses for these sizes.
+// Bytes of workspace launch_fp4_attention needs for these sizes; with `uneven`
+// what it can use where some sequences are much longer than others.
 int64_t fp4_attention_workspace(int64_t batch, int64_t num_tokens, int32_t q_heads,
-                                int32_t kv_heads, int32_t dim);
+                                int32_t kv_heads, int32_t dim, bool uneven);
 cudaError_t launch_fp4_attention(const Fp4Attention &a, cudaStream_t stream);
 
 // Its kernel for many rows to a KV head (fp4_attention_rows.cu).
 bool fp4_attention_by_rows(int64_t batch, int64_t num_tokens, int32_t group);
-int64_t fp4_attention_rows_workspace(int64_t num_tokens, int32_t group, int32_t kv_heads,
-                                     int32_t dim);
+int64_t fp4_attention_rows_workspace(int64_t num_tokens, int32_t group, int32_t kv_heads, int32_t dim,
+                                     bool uneven);
 cudaError_t launch_fp4_attention_rows(const Fp4Attention &a, cudaStream_t stream);
 
 struct QkNormRope {

@@ -28,7 +28,8 @@ struct Division {
     int32_t sets;        // sets of KV heads
     int32_t unit;        // cached tokens of a unit
     int32_t window;
-    int32_t whole;       // items are not split: 0 or 1
+    int32_t whole;       // 0: items are split where runs end; 1: they are not;
+                         // 2: only those that cost more than a run
 };
 
 // One sequence as the kernels see it: bad lengths and ranges are cut to what
