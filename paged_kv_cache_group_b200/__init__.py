@@ -404,23 +404,26 @@ except ImportError:
     _current_device = torch.cuda.current_device
 
 
-def _rows3(t: torch.Tensor, name: str) -> int:
-    """Row stride in elements of a CUDA bf16 ``[T, heads, dim]`` tensor whose
-    rows are contiguous."""
-    if t.dtype != torch.bfloat16 or not t.is_cuda:
+_BF16, _U8, _I32, _I64, _F32 = torch.bfloat16, torch.uint8, torch.int32, torch.int64, torch.float32
+
+
+def _rows3(t: torch.Tensor, shape, name: str) -> int:
+    """Row stride in elements of a CUDA bf16 ``[T, heads, dim]`` tensor of this
+    shape whose rows are contiguous."""
+    if t.dtype != _BF16 or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA bfloat16 tensor")
-    n, heads, dim = t.shape
+    n, heads, dim = shape
     s0, s1, s2 = t.stride()
-    if (s2 != 1 and dim != 1) or (s1 != dim and heads != 1):
-        if t.numel():
+    if s1 != dim or s2 != 1:
+        if ((s2 != 1 and dim != 1) or (s1 != dim and heads != 1)) and t.numel():
             raise ValueError(f"{name} rows must be contiguous")
     return s0 if n > 1 else heads * dim
 
 
-def _same_device(device: int, names: tuple, tensors: tuple) -> None:
+def _same_device(device: int, names: str, *tensors) -> None:
     for i, t in enumerate(tensors):
         if t is not None and t.get_device() != device:
-            raise ValueError(f"{names[i]} must be on the same CUDA device as the other tensors")
+            raise ValueError(f"{names.split()[i]} must be on the same CUDA device as the other tensors")
 
 
 def _call_on(device: int, stream, name: str, fn, *args) -> None:
@@ -435,7 +438,7 @@ def _call_on(device: int, stream, name: str, fn, *args) -> None:
     else:
         with torch.cuda.device(device):
             status = fn(*args, raw)
-    if status != _abi.OK:
+    if status:
         _check(name, status)
 
 
@@ -459,8 +462,7 @@ def fp4_kv_pools(num_blocks: int, block_size: int, num_kv_heads: int, head_dim: 
 def _fp4_geometry(k_pool: torch.Tensor, v_pool: torch.Tensor):
     """Pools ``[num_blocks, heads, block_size / 16, 9 * dim]`` (block stride may
     be padded): (num_blocks, heads, block_size, dim, block stride in bytes)."""
-    if k_pool.dtype != torch.uint8 or v_pool.dtype != torch.uint8 or not k_pool.is_cuda \
-            or not v_pool.is_cuda:
+    if k_pool.dtype != _U8 or v_pool.dtype != _U8 or not k_pool.is_cuda or not v_pool.is_cuda:
         raise TypeError("k_pool and v_pool must be CUDA uint8 tensors")
     shape, stride = k_pool.shape, k_pool.stride()
     if shape != v_pool.shape or stride != v_pool.stride():
@@ -478,19 +480,20 @@ def _fp4_geometry(k_pool: torch.Tensor, v_pool: torch.Tensor):
 def _fp4_rows(k: torch.Tensor, v: torch.Tensor, slot_mapping, k_pool, v_pool, scale_dev):
     """Shared argument checks of fp4_kv_write and fp4_kv_read; their arguments
     up to the scales."""
-    if k.dim() != 3 or k.shape != v.shape:
+    shape = k.shape
+    if len(shape) != 3 or shape != v.shape:
         raise ValueError(f"k and v must both be [T, heads, dim] of one shape, got {tuple(k.shape)} "
                          f"and {tuple(v.shape)}")
-    ks, vs = _rows3(k, "k"), _rows3(v, "v")
-    t, heads, dim = k.shape
+    ks, vs = _rows3(k, shape, "k"), _rows3(v, shape, "v")
+    t, heads, dim = shape
     _check_slots(slot_mapping, t)
     _check_scale_pair(scale_dev, "scale_dev")
     nb, pool_heads, bs, pool_dim, stride = _fp4_geometry(k_pool, v_pool)
     if (heads, dim) != (pool_heads, pool_dim):
         raise ValueError(f"pools hold {pool_heads} heads of {pool_dim}, k and v have {heads} of {dim}")
     device = k.get_device()
-    _same_device(device, ("v", "k_pool", "v_pool", "scale_dev", "slot_mapping"),
-                 (v, k_pool, v_pool, scale_dev, slot_mapping if t else None))
+    _same_device(device, "v k_pool v_pool scale_dev slot_mapping", v, k_pool, v_pool, scale_dev,
+                 slot_mapping if t else None)
     return device, (k.data_ptr(), v.data_ptr(), ks, vs, slot_mapping.data_ptr(), t, heads, dim,
                     k_pool.data_ptr(), v_pool.data_ptr(), bs, stride, nb)
 
@@ -540,7 +543,7 @@ def _allocating_for(stream, device: torch.device):
 
 
 def _check_index(t: torch.Tensor, name: str, *shape) -> None:
-    if t.dtype != torch.int32 or tuple(t.shape) != shape:
+    if t.dtype != _I32 or t.shape != shape:
         raise ValueError(f"{name} must be int32 {list(shape)}")
 
 
@@ -575,21 +578,25 @@ def fp4_kv_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor
     [T, q_heads]`` is given to be filled.  ``workspace`` (uint8, at least
     fp4_kv_attention_workspace() bytes) is allocated for the call when not
     given, for sequences of any lengths; calls that may overlap need one each."""
-    if q.dim() != 3:
+    shape = q.shape
+    if len(shape) != 3:
         raise ValueError("q must be [T, heads, dim]")
-    q_stride = _rows3(q, "q")
-    t, q_heads, dim = q.shape
+    q_stride = _rows3(q, shape, "q")
+    t, q_heads, dim = shape
     nb, heads, bs, pool_dim, stride = _fp4_geometry(k_pool, v_pool)
     if dim != pool_dim or heads == 0 or q_heads % heads:
         raise ValueError(f"pools hold {heads} heads of {pool_dim}, q has {q_heads} of {dim}")
     batch = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
     _check_index(seq_lens, "seq_lens", batch)
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != batch:
+    table_shape = block_table.shape
+    if block_table.dtype != _I32 or len(table_shape) != 2 or table_shape[0] != batch:
         raise ValueError("block_table must be int32 [batch, width]")
-    width = block_table.shape[1]
-    if block_table.stride(1) != 1 and width > 1:
+    width = table_shape[1]
+    table_stride, step = block_table.stride()
+    if step != 1 and width > 1:
         raise ValueError("block_table rows must be contiguous")
-    table_stride = block_table.stride(0) if batch > 1 else width
+    if batch <= 1:
+        table_stride = width
     if batch > 1 and seq_lens.stride(0) != 1:
         raise ValueError("seq_lens must be contiguous")
     if q_start is not None:
@@ -603,21 +610,20 @@ def fp4_kv_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor
     if out is None or workspace is None:
         with _allocating_for(stream, q.device):
             if out is None:
-                out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+                out = torch.empty(shape, dtype=_BF16, device=q.device)
             if workspace is None:
                 workspace = torch.empty(fp4_kv_attention_workspace(batch, t, q_heads, heads, dim, True),
-                                        dtype=torch.uint8, device=q.device)
-    if out.shape != q.shape:
+                                        dtype=_U8, device=q.device)
+    if out.shape != shape:
         raise ValueError("out must have the shape of q")
-    out_stride = _rows3(out, "out")
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (t, q_heads)
+    out_stride = _rows3(out, shape, "out")
+    if lse is not None and (lse.dtype != _F32 or lse.shape != (t, q_heads)
                             or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 tensor [T, q_heads]")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    _same_device(device, ("k_pool", "v_pool", "block_table", "seq_lens", "q_start", "scale_dev", "out",
-                          "lse", "workspace"),
-                 (k_pool, v_pool, block_table, seq_lens, q_start, scale_dev, out, lse, workspace))
+    _same_device(device, "k_pool v_pool block_table seq_lens q_start scale_dev out lse workspace",
+                 k_pool, v_pool, block_table, seq_lens, q_start, scale_dev, out, lse, workspace)
     _call_on(device, stream, "fp4_kv_attention", lib.fp4_kv_attention,
              q.data_ptr(), q_stride, k_pool.data_ptr(), v_pool.data_ptr(), bs, stride, nb, heads,
              dim, block_table.data_ptr(), table_stride, width, seq_lens.data_ptr(), _ptr(q_start),
@@ -675,33 +681,32 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor,
     ``positions[t] * inv_freq`` (fp64): halves paired, or neighbours when
     ``interleaved``.  ``rope_scale`` multiplies cosine and sine.  ``q_out`` and
     ``k_out`` may be ``q`` and ``k``."""
-    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+    q_shape, k_shape = q.shape, k.shape
+    if len(q_shape) != 3 or len(k_shape) != 3 or q_shape[0] != k_shape[0] or q_shape[2] != k_shape[2]:
         raise ValueError(f"q and k must be [T, heads, dim] with the same T and dim, got "
                          f"{tuple(q.shape)} and {tuple(k.shape)}")
-    q_stride, k_stride = _rows3(q, "q"), _rows3(k, "k")
-    t, q_heads, dim = q.shape
-    k_heads = k.shape[1]
-    if positions.dtype != torch.int64 or tuple(positions.shape) != (t,) or \
-            (t > 1 and positions.stride(0) != 1):
+    q_stride, k_stride = _rows3(q, q_shape, "q"), _rows3(k, k_shape, "k")
+    t, q_heads, dim = q_shape
+    k_heads = k_shape[1]
+    if positions.dtype != _I64 or positions.shape != (t,) or (t > 1 and positions.stride(0) != 1):
         raise ValueError("positions must be a contiguous int64 tensor [T]")
     if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous float64 tensor [rotary_dim / 2]")
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None and (w.dtype != torch.bfloat16 or tuple(w.shape) != (dim,)
-                              or not w.is_contiguous()):
+        if w is not None and (w.dtype != _BF16 or w.shape != (dim,) or not w.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous bfloat16 tensor [dim]")
     device = q.get_device()
     if q_out is None or k_out is None:
         with _allocating_for(stream, q.device):
             if q_out is None:
-                q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+                q_out = torch.empty(q_shape, dtype=_BF16, device=q.device)
             if k_out is None:
-                k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
-    if q_out.shape != q.shape or k_out.shape != k.shape:
+                k_out = torch.empty(k_shape, dtype=_BF16, device=q.device)
+    if q_out.shape != q_shape or k_out.shape != k_shape:
         raise ValueError("q_out and k_out must have the shapes of q and k")
-    qo_stride, ko_stride = _rows3(q_out, "q_out"), _rows3(k_out, "k_out")
-    _same_device(device, ("k", "positions", "inv_freq", "q_weight", "k_weight", "q_out", "k_out"),
-                 (k, positions, inv_freq, q_weight, k_weight, q_out, k_out))
+    qo_stride, ko_stride = _rows3(q_out, q_shape, "q_out"), _rows3(k_out, k_shape, "k_out")
+    _same_device(device, "k positions inv_freq q_weight k_weight q_out k_out", k, positions, inv_freq,
+                 q_weight, k_weight, q_out, k_out)
     _call_on(device, stream, "qk_norm_rope", lib.qk_norm_rope,
              q.data_ptr(), k.data_ptr(), q_stride, k_stride, q_out.data_ptr(), k_out.data_ptr(),
              qo_stride, ko_stride, positions.data_ptr(), inv_freq.data_ptr(), _ptr(q_weight),
