@@ -20,11 +20,11 @@ constexpr uint32_t kFp4ErrScale = 0x2u;
 constexpr uint32_t kFp4ErrSequence = 0x4u;
 constexpr uint32_t kFp4ErrWait = 0x8u;
 
-// Launch with programmatic stream serialization: the kernel may be scheduled
-// while the one before it on the stream runs, and waits for it itself.
+// Launch; if `early` with programmatic stream serialization: the kernel may be
+// scheduled while the one before it on the stream runs, and waits for it itself.
 template <typename... Params, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, int block, size_t smem,
-                       cudaStream_t stream, Args &&...args) {
+cudaError_t launch_when(bool early, void (*kernel)(Params...), dim3 grid, int block, size_t smem,
+                        cudaStream_t stream, Args &&...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(static_cast<unsigned>(block));
@@ -34,11 +34,17 @@ cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, int block, size_t s
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = early ? 1 : 0;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e == cudaSuccess) g_launch_count.fetch_add(1, std::memory_order_relaxed);
     return e;
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, int block, size_t smem,
+                       cudaStream_t stream, Args &&...args) {
+    return launch_when(true, kernel, grid, block, smem, stream, std::forward<Args>(args)...);
 }
 
 // Multiprocessors of the current device.
