@@ -999,7 +999,8 @@ __global__ void __launch_bounds__(32 * kFewWarps) fp4_attention_join_few_kernel(
 
 // Rows of a tile (8 * NT) for an average of `rows` rows a sequence: the
 // smallest tile that holds them, up to what the accumulators leave room for
-// in registers (NT * D <= 256).
+// in registers (NT * D <= 256; 24 rows of 128 spilled, and took 60 us for 32
+// drafts of 5 to 40 rows where 16 rows at a time take 36).
 int tiles_of(int64_t batch, int64_t num_tokens, int32_t group, int32_t dim) {
     const int64_t rows = (num_tokens + batch - 1) / batch * group;
     return rows <= 8 || dim == 256 ? 1 : 2;
@@ -1084,13 +1085,13 @@ cudaError_t launch_heads(const Fp4Attention &a, cudaStream_t stream) {
 
 }  // namespace
 
-// More than 36 rows a sequence on average: their tiles are shared.  Measured
-// with 32 sequences of 1000-3000 tokens and 8 heads of 64, 128 and 256, this
-// kernel against the one by rows: 30 rows 38, 56 and 117 us against 46, 67 and
-// 145; 40 rows 49, 75 and 150 against 50, 71 and 147; 60 rows 60, 95 and 217
-// against 51, 73 and 148.
+// More than 32 rows a sequence on average: their tiles are shared.  Measured
+// with 32 sequences of 1000-3000 tokens and 8 heads of 64 and 128, this kernel
+// against the one by rows: 30 rows 39 and 54 us against 46 and 65; 35 rows
+// (three tiles) 51 and 72 against 49 and 69; 60 rows 60 and 95 against 51 and
+// 73.  With 256, 30 rows 117 against 145, 40 rows 150 against 147.
 bool fp4_attention_by_rows(int64_t batch, int64_t num_tokens, int32_t group) {
-    return num_tokens * group > 36 * batch;
+    return num_tokens * group > 32 * batch;
 }
 
 int64_t fp4_attention_workspace(int64_t batch, int64_t num_tokens, int32_t q_heads,
