@@ -32,13 +32,18 @@
 // product for each pair of codes; the rest is kept off the four warps that do
 // it.  A fifth warp looks up pages and copies tiles ahead of them, across the
 // items of the block too, so that the next sequence's tokens are under way
-// while this one's sums are finished.  It is the copies that have to be few:
-// of 1152 bytes each (16 tokens of one head of 128) the copying warps kept
-// 4.1 TB/s whether or not anything was computed.  So a block takes four, two or one
-// heads at once, with one, two or four of its warps on each: the heads of a page lie side by side, and one copy takes all
-// of them when a page is 16 tokens, or 32 tokens of one when it is longer.
-// The running maximum is joined over lanes only when some lane sees a larger
-// score.
+// while this one's sums are finished.  Its copies have to be few: a lane's
+// copies are issued one after the other.  So a block takes four, two or one
+// heads at once, with one, two or four of its warps on each: the heads of a
+// page lie side by side, and one copy takes all of them when a page is 16
+// tokens, or 32 tokens of one when it is longer.  The running maximum is joined
+// over lanes only when some lane sees a larger score.
+//
+// Measured, 256 sequences of 3001-6000 tokens x 4 heads of 128 (664 MB):
+// 132 us with the join, 5.0 TB/s; the kernel alone 126, of which its copies
+// alone would take 109 and its arithmetic alone 107 (158 us with a copy for
+// each head).  One sequence of 200003 tokens 38 us, of which 9000 cycles pass
+// before the first product and 6 us in the join.
 #include <cuda_runtime.h>
 
 #include <cmath>

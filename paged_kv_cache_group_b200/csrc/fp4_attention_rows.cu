@@ -16,9 +16,14 @@
 // other's gaps (one with 256 dimensions).  The next scores are formed before
 // this tile's weights are used, where tensor memory holds both.
 //
-// Bound by the latency of a tile's chain (scores, softmax, weights, product)
-// and the exponentials in it: a warp alone takes 8 cycles for each, four of a
-// scheduler 4.6, which is why a row has two threads.
+// Bound by the latency of a tile's chain (scores, softmax, weights, product),
+// about 3700 cycles for a tile in each of the two blocks, and the exponentials
+// in it: one warp of a scheduler takes 12 cycles for a score, four of them 4.8
+// each, which is why a row has two threads.
+//
+// Measured, 4 pieces of 200-500 tokens x 48 heads of 64 on 2000-4001 cached
+// tokens with a window of 1024 (14.4 GFLOP): 59 us, 242 TFLOP/s; 105 us with
+// the kernel for few rows.
 //
 // Operands are exact as there: code * block scale in fp16, and a query row
 // scaled by a power of two.  The scores are taken against a reference that
