@@ -8,7 +8,7 @@
 
 namespace fp8q {
 
-constexpr int32_t kWaitTries = 200000;  // polls of a barrier before giving up
+constexpr int32_t kWaitTries = 1 << 20;   // polls of a barrier before giving up
 constexpr uint32_t kSleepNs = 20000;    // of one poll, at most
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;

@@ -212,3 +212,23 @@ def test_pools_past_two_to_the_31_bytes():
         near = fp8q.fp4_kv_attention(rows.cuda(), *small, table - (blocks - 40), lens_dev, q_start=start)
         assert torch.equal(far, near) and bool(torch.isfinite(far).all()) and bool(far.any())
     assert fp8q.fp8q_device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("news,cls", [(1, Batch), (70, Many)])
+def test_few_live_sequences_among_many_empty_ones(news, cls):
+    count, live = 4000, (0, 1777, 3999)
+    lens, new = [0] * count, [0] * count
+    for i, b in enumerate(live):
+        lens[b], new[b] = 90 + 60 * i, news
+    b = cls(38, 64, 2, 2, 16, lens, new)
+    b.check(*b.call())
+
+
+def test_only_empty_sequences():
+    b = Batch(39, 64, 2, 2, 16, [0, 7, 0], [0, 0, 0], spare=4)
+    out, lse = b.call()
+    assert bool((out == 3.0).all()) and bool((lse == 3.0).all())
+    b = Batch(40, 64, 2, 40, 16, [0, 0], [40, 30])           # new tokens of sequences without any cached
+    out, lse = b.call()
+    assert not bool(out.any()) and bool(torch.isneginf(lse).all())
+    assert fp8q.fp8q_device_error(clear=True) == 0
