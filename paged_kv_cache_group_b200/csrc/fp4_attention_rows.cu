@@ -347,6 +347,7 @@ __device__ __forceinline__ void issue_items(Shared<D> &sm, const Waits &wait, ui
             __syncwarp();
         };
         wait(sm.c.k_full, n);
+        if (!L::kApart && n > 0) wait(sm.c.summed, n - 1);   // the last weights lie where the scores go
         scores();
         for (int32_t j = 0; j < tiles; ++j, ++n) {
             // The weights come last; nothing else is waited for behind them.
@@ -473,38 +474,98 @@ __device__ __forceinline__ float other_half(Control &c, int32_t half, int32_t ro
     return v;
 }
 
-// A row of an item that is behind the products, for the output.
-struct Done {
+// A thread's row of an item.
+struct Mine {
+    int32_t tiles;              // as in Item
+    int32_t begin, part;
+    bool busy, live;            // the warp has rows; the row is one of them
     RowPlace place;
-    int32_t part;        // as in Item; -2: nothing to put out
-    bool tiles;
-    float ref, sum;
+    float c;                    // factor of raw scores: log2 of a weight
+    int32_t hi, lo;             // tokens the row sees: [lo, hi)
+    int32_t all_hi, all_lo;     // ... and all rows of the warp
 };
 
+// The next item: its query rows go to shared memory once the last product with
+// the present ones is done, which the caller knows.
 template <int D>
-__device__ __forceinline__ void put_out(const Fp4Attention &a, const Done &done, uint32_t t_sums, int32_t half,
-                                        int32_t row, bool live, float v_scale) {
+__device__ __forceinline__ Mine take_item(const Fp4Attention &a, Shared<D> &sm, const Waits &wait, uint32_t items,
+                                          int32_t group, float k_scale) {
+    constexpr int kPieces = D / 16;                    // 16-byte pieces of half a query row
+    const int32_t half = threadIdx.x / 128, row = threadIdx.x % 128;
+    wait(sm.c.item_full[items % 2], items / 2);
+    const Item it = sm.c.item[items % 2];
+    warp_arrive(sm.c.item_empty[items % 2]);
+    Mine m;
+    m.tiles = it.tiles;
+    m.begin = it.begin;
+    m.part = it.part;
+    m.busy = row / 32 * 32 < it.rows && it.tiles >= 0;
+    m.live = row < it.rows;
+    m.c = 1.0f;
+    if (it.tiles < 0) return m;
+    const int32_t my_row = it.row0 + min(row, it.rows - 1);
+    m.place = row_place(it.token0, my_row, it.head, group);
+    const int32_t p = it.ahead + (m.place.token - it.token0) + 1;
+    m.hi = min(it.end, p);
+    m.lo = a.window > 0 ? max(0, p - a.window) : 0;
+    m.all_hi = __reduce_min_sync(0xFFFFFFFFu, m.hi);
+    m.all_lo = __reduce_max_sync(0xFFFFFFFFu, m.lo);
+    if (it.tiles == 0) return m;
+    if (m.busy) {
+        uint4 x[kPieces];                              // this half of the query row
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            a.q + m.place.token * a.q_stride + static_cast<int64_t>(m.place.q_head) * D) + half * kPieces;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) x[i] = src[i];
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) most = max(most, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+        }
+        most = max(most, __float_as_uint(other_half(sm.c, half, row, __uint_as_float(most))));
+        const int32_t up = min(8 - (static_cast<int32_t>(most >> 7) - 127), 120);
+        const float scale = m.live ? __int_as_float((127 + up) << 23) : 0.0f;
+        m.c = fmaxf(a.softmax_scale * kLog2e * k_scale * __int_as_float((127 - up) << 23), 0x1p-100f);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+            *reinterpret_cast<uint4 *>(sm.q + piece_at(row, half * kPieces + i)) =
+                make_uint4(f16x2_of(bf16_low(x[i].x) * scale, bf16_high(x[i].x) * scale),
+                           f16x2_of(bf16_low(x[i].y) * scale, bf16_high(x[i].y) * scale),
+                           f16x2_of(bf16_low(x[i].z) * scale, bf16_high(x[i].z) * scale),
+                           f16x2_of(bf16_low(x[i].w) * scale, bf16_high(x[i].w) * scale));
+    }
+    operands_written();
+    warp_arrive(sm.c.q_full);
+    return m;
+}
+
+// The output of a row, or its part.
+template <int D>
+__device__ __forceinline__ void put_out(const Fp4Attention &a, const Mine &m, float ref, float sum, uint32_t t_sums,
+                                        int32_t half, int32_t row, float v_scale) {
     using L = Layout<D>;
-    float *part = part_at(a.workspace, 2 * static_cast<int64_t>(blockIdx.x) + max(done.part, 0), L::kPartFloats);
-    const float inv = row_factor(done.sum, v_scale);
-    uint4 *out = reinterpret_cast<uint4 *>(a.out + done.place.token * a.out_stride +
-                                           static_cast<int64_t>(done.place.q_head) * D);
+    float *part = part_at(a.workspace, 2 * static_cast<int64_t>(blockIdx.x) + max(m.part, 0), L::kPartFloats);
+    const float inv = row_factor(sum, v_scale);
+    uint4 *out = reinterpret_cast<uint4 *>(a.out + m.place.token * a.out_stride +
+                                           static_cast<int64_t>(m.place.q_head) * D);
 #pragma unroll 2
     for (int q = half * (D / 32); q < (half + 1) * (D / 32); ++q) {
         float o[16];
-        if (done.tiles) {
+        if (m.tiles > 0) {
             tmem_load(t_sums + 16 * q, o);
             tmem_wait_load();
         } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[i] = 0.0f;
         }
-        if (done.part >= 0) {                          // [dimensions / 4][rows]
+        if (m.part >= 0) {                             // [dimensions / 4][rows]
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 reinterpret_cast<float4 *>(part)[(4 * q + i) * kRows + row] =
                     make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-        } else if (live) {
+        } else if (m.live) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 out[2 * q + i] = make_uint4(bf16x2_of(o[8 * i] * inv, o[8 * i + 1] * inv),
@@ -514,12 +575,11 @@ __device__ __forceinline__ void put_out(const Fp4Attention &a, const Done &done,
         }
     }
     if (half == 0) {
-        if (done.part >= 0) {
-            part[kRows * D + row] = done.ref;
-            part[kRows * D + kRows + row] = done.sum;
-        } else if (live && a.lse != nullptr) {
-            a.lse[static_cast<int64_t>(done.place.token) * a.q_heads + done.place.q_head] =
-                row_lse(done.ref, done.sum, kShift);
+        if (m.part >= 0) {
+            part[kRows * D + row] = ref;
+            part[kRows * D + kRows + row] = sum;
+        } else if (m.live && a.lse != nullptr) {
+            a.lse[static_cast<int64_t>(m.place.token) * a.q_heads + m.place.q_head] = row_lse(ref, sum, kShift);
         }
     }
     tmem_before();                                     // the sums have been read
@@ -529,67 +589,16 @@ template <int D>
 __device__ __forceinline__ void softmax_items(const Fp4Attention &a, Shared<D> &sm, const Waits &wait,
                                               uint32_t tmem, int32_t group, float k_scale, float v_scale) {
     using L = Layout<D>;
-    constexpr int kPieces = D / 16;                    // 16-byte pieces of half a query row
     const int32_t half = threadIdx.x / 128, row = threadIdx.x % 128, quarter = row / 32;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t t_sums = tmem + lanes + L::kSumsAt;
     const uint32_t t_scores = tmem + lanes + kColumns * half;
     const uint32_t t_weights = tmem + lanes + L::kWeightsAt + L::kWeightsHalf * half;
-    uint32_t n = 0;
-    Done done;
-    done.part = -2;
-    bool was_live = false;
-    for (uint32_t items = 0;; ++items) {
-        wait(sm.c.item_full[items % 2], items / 2);
-        const Item it = sm.c.item[items % 2];
-        warp_arrive(sm.c.item_empty[items % 2]);
-        const bool busy = quarter * 32 < it.rows && it.tiles >= 0;   // the warp has rows
-        const bool live = row < it.rows;
-        const int32_t my_row = it.row0 + min(row, it.rows - 1);
-        const RowPlace place = row_place(it.token0, my_row, it.head, group);
-        uint4 x[kPieces];                              // this half of the query row
-        if (busy && it.tiles > 0) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(
-                a.q + place.token * a.q_stride + static_cast<int64_t>(place.q_head) * D) + half * kPieces;
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i) x[i] = src[i];
-        }
-        // The last item's output, while the query rows come.
-        if (done.part > -2) put_out<D>(a, done, t_sums, half, row, was_live, v_scale);
-        if (it.tiles < 0) return;
-        done.part = -2;
-        was_live = live;
-        float c = 1.0f;                                // factor of raw scores: log2 of a weight
-        if (busy && it.tiles > 0) {
-            uint32_t most = 0;
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) most = max(most, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
-            }
-            most = max(most, __float_as_uint(other_half(sm.c, half, row, __uint_as_float(most))));
-            const int32_t up = min(8 - (static_cast<int32_t>(most >> 7) - 127), 120);
-            const float scale = live ? __int_as_float((127 + up) << 23) : 0.0f;
-            c = fmaxf(a.softmax_scale * kLog2e * k_scale * __int_as_float((127 - up) << 23), 0x1p-100f);
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i)
-                *reinterpret_cast<uint4 *>(sm.q + piece_at(row, half * kPieces + i)) =
-                    make_uint4(f16x2_of(bf16_low(x[i].x) * scale, bf16_high(x[i].x) * scale),
-                               f16x2_of(bf16_low(x[i].y) * scale, bf16_high(x[i].y) * scale),
-                               f16x2_of(bf16_low(x[i].z) * scale, bf16_high(x[i].z) * scale),
-                               f16x2_of(bf16_low(x[i].w) * scale, bf16_high(x[i].w) * scale));
-        }
-        if (it.tiles > 0) {
-            operands_written();
-            warp_arrive(sm.c.q_full);
-        }
-        // tokens this row sees, and those all rows of the warp see
-        const int32_t p = it.ahead + my_row / group + 1;
-        const int32_t hi = min(it.end, p), lo = a.window > 0 ? max(0, p - a.window) : 0;
-        const int32_t all_hi = __reduce_min_sync(0xFFFFFFFFu, hi), all_lo = __reduce_max_sync(0xFFFFFFFFu, lo);
+    uint32_t n = 0, items = 0;
+    Mine m = take_item<D>(a, sm, wait, items, group, k_scale);
+    while (m.tiles >= 0) {
         float ref = -INFINITY, sum = 0.0f;
-        for (int32_t j = 0; j < it.tiles; ++j, ++n) {
+        for (int32_t j = 0; j < m.tiles; ++j, ++n) {
             wait(sm.c.scores, n);
             __syncwarp();
             tmem_after();
@@ -601,14 +610,14 @@ __device__ __forceinline__ void softmax_items(const Fp4Attention &a, Shared<D> &
                 __syncwarp();
                 tmem_after();
             };
-            if (!busy) summed();
-            if (busy) {
-                const int32_t base = it.begin + j * kTokens;
-                const bool edge = base + kTokens > all_hi || base < all_lo;
+            if (!m.busy) summed();
+            if (m.busy) {
+                const int32_t base = m.begin + j * kTokens;
+                const bool edge = base + kTokens > m.all_hi || base < m.all_lo;
                 // columns this row sees, of this thread's
-                const int32_t from = lo - base - kColumns * half, to = max(from, hi - base - kColumns * half);
+                const int32_t from = m.lo - base - kColumns * half, to = max(from, m.hi - base - kColumns * half);
                 float top = edge ? row_max<true>(t_scores, from, to) : row_max<false>(t_scores, from, to);
-                top = fmaxf(top, other_half(sm.c, half, row, top)) * c;
+                top = fmaxf(top, other_half(sm.c, half, row, top)) * m.c;
                 // The reference moves where a row of the warps has outgrown it.
                 if (__any_sync(0xFFFFFFFFu, top > ref + kSlack)) {
                     const float now = fmaxf(ref, top);
@@ -630,25 +639,26 @@ __device__ __forceinline__ void softmax_items(const Fp4Attention &a, Shared<D> &
                 }
                 const float against = kShift - (ref == -INFINITY ? 0.0f : ref);
                 summed();
-                sum += edge ? row_weights<true>(t_scores, t_weights, from, to, c, against)
-                            : row_weights<false>(t_scores, t_weights, from, to, c, against);
+                sum += edge ? row_weights<true>(t_scores, t_weights, from, to, m.c, against)
+                            : row_weights<false>(t_scores, t_weights, from, to, m.c, against);
                 tmem_wait_store();
             }
             tmem_before();
             warp_arrive(sm.c.weights);
         }
-        if (it.tiles > 0) {
+        // The next item's rows are put in place while this one's last product
+        // runs, and its first scores are formed while these sums are put out.
+        const Mine next = take_item<D>(a, sm, wait, ++items, group, k_scale);
+        if (m.tiles > 0) {
             wait(sm.c.summed, n - 1);
             __syncwarp();
             tmem_after();
         }
-        if (!busy) continue;
-        sum += other_half(sm.c, half, row, sum);
-        done.place = place;
-        done.part = it.part;
-        done.tiles = it.tiles > 0;
-        done.ref = ref;
-        done.sum = sum;
+        if (m.busy) {
+            sum += other_half(sm.c, half, row, sum);
+            put_out<D>(a, m, ref, sum, t_sums, half, row, v_scale);
+        }
+        m = next;
     }
 }
 
