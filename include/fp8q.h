@@ -638,8 +638,9 @@ FP8Q_API fp8q_status fp4_kv_read(void *k, void *v, int64_t key_stride, int64_t v
  * A row that sees no token gets out = 0 and lse = -infinity.  Rows of q that no
  * sequence has keep what out and lse held.  Scores, sums and outputs are fp32,
  * rounded once to bf16; the softmax weights are rounded to fp16 for the second
- * product.  The result does not depend on what unused slots hold, and is the
- * same in every run on one kind of GPU.
+ * product.  A NaN in a query row reaches that row's outputs alone.  The result
+ * does not depend on what unused slots hold, and is the same in every run on one
+ * kind of GPU.
  *
  * The lengths and tables are read on the device, and the launches depend on
  * the sizes alone: a captured call may be replayed with other contents.  A

@@ -2,10 +2,9 @@
 //
 // An item is one (sequence, set of KV heads, tile of query rows).  It is made
 // of units of some cached tokens, counted from the first token its own rows
-// see, and costs its units plus kItemCost: loading the rows and finishing the
-// sums take about as long as a unit.  Items are laid side by side on one axis, every
-// block takes an equal run of it, and unit j of an item lies at the point
-// item start + kItemCost + j.  A block finds its run from the lengths on the
+// see, and costs its units plus what loading its rows and finishing its sums take,
+// in units.  Items are laid side by side on one axis, every block takes an equal
+// run of it, and unit j of an item lies at the point item start + that cost + j.  A block finds its run from the lengths on the
 // device, so a launch depends on sizes alone and may be captured.
 //
 // An item whose units lie in several blocks leaves one part in each: blocks
@@ -18,7 +17,6 @@
 namespace fp8q {
 namespace fp4_plan {
 
-constexpr int kItemCost = 1;           // units an item costs beside its own
 constexpr int kMaxBlocks = 444;        // blocks a workspace has room for
 
 // How a kernel divides its work.
@@ -27,6 +25,7 @@ struct Division {
     int32_t tile_rows;   // rows of a tile
     int32_t sets;        // sets of KV heads
     int32_t unit;        // cached tokens of a unit
+    int32_t item_cost;   // units an item costs beside its own
     int32_t window;
     int32_t whole;       // 0: items are split where runs end; 1: they are not;
                          // 2: only those that cost more than a run
@@ -106,7 +105,7 @@ __device__ __forceinline__ int64_t set_cost(const Sequence &mine, const Division
     int64_t cost = 0;
     if (mine.row_tiles <= kFew)
         for (int32_t rt = 0; rt < mine.row_tiles; ++rt)
-            cost += tile_of(mine, d, rt).units + kItemCost;
+            cost += tile_of(mine, d, rt).units + d.item_cost;
     for (uint32_t many = __ballot_sync(0xFFFFFFFFu, mine.row_tiles > kFew); many; many &= many - 1) {
         const int32_t from = __ffs(many) - 1;
         Sequence s;
@@ -116,7 +115,7 @@ __device__ __forceinline__ int64_t set_cost(const Sequence &mine, const Division
         s.row_tiles = __shfl_sync(0xFFFFFFFFu, mine.row_tiles, from);
         int64_t sum = 0;
         for (int32_t rt = lane; rt < s.row_tiles; rt += 32)
-            sum += tile_of(s, d, rt).units + kItemCost;
+            sum += tile_of(s, d, rt).units + d.item_cost;
 #pragma unroll
         for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
         if (lane == from) cost = sum;
@@ -222,7 +221,7 @@ struct Walk {
         for (int32_t first = 0; s.row_tiles > 1; first += 32) {   // the tile that holds r.at
             int32_t n = 0;
             if (first + lane < s.row_tiles)
-                n = tile_of(s, d, first + lane).units + kItemCost;
+                n = tile_of(s, d, first + lane).units + d.item_cost;
             int64_t incl = n;
 #pragma unroll
             for (int o = 1; o < 32; o *= 2) {
