@@ -13,6 +13,19 @@ constexpr uint32_t kSleepNs = 20000;    // of one poll, at most
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
+// The log2 of a weight is c * raw score - maximum + shift, with raw scores below
+// 2^9 * 2688 * D.  One multiply-add for it takes the roundings of the maximum,
+// with the shift and without it, into the exponent whole: half a bit where
+// c * raw is 2^22 and any number of bits beyond, past what fp16 holds or down to
+// no weight at all.  Rows whose c allows 2^21 have the maximum subtracted first,
+// from the rounded product, which leaves the largest score at the shift exactly.
+// That goes by the row alone: rows beside it are what they are beside any other.
+template <int D>
+__device__ __forceinline__ bool in_steps(float c) { return !(c <= 0x1p21f / (512.0f * 2688.0f * D)); }
+__device__ __forceinline__ float below_most(float raw, float c, float most) {
+    return __fsub_rn(__fmul_rn(raw, c), most);
+}
+
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }

@@ -498,6 +498,10 @@ __device__ __forceinline__ void compute_items(const Fp4Attention &a, Shared<D, N
 
         float c[NT][2];
         prepare_rows<D, NT, T>(a, it.rows, sm.q[slot][hh], k_scale, c);
+        bool steps = false;                        // some row's weights are formed in steps
+#pragma unroll
+        for (int n = 0; n < NT; ++n) steps |= in_steps<D>(c[n][0]) || in_steps<D>(c[n][1]);
+        steps = __any_sync(0xFFFFFFFFu, steps);
         const uint4 *rows = reinterpret_cast<const uint4 *>(sm.q[slot][hh]);
         float top[NT][2], ref[NT][2], sum[NT][2];  // ref: what scores are taken against
         float o[S::kMTiles][NT][4];
@@ -553,7 +557,7 @@ __device__ __forceinline__ void compute_items(const Fp4Attention &a, Shared<D, N
                                                  fmaxf(sc[1][n][j], sc[1][n][2 + j]));
                     grew |= mx[n][j] > top[n][j];
                 }
-            if (__any_sync(0xFFFFFFFFu, grew)) {
+            if (__any_sync(0xFFFFFFFFu, grew) || steps) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float shrink[2];
@@ -575,6 +579,25 @@ __device__ __forceinline__ void compute_items(const Fp4Attention &a, Shared<D, N
                     for (int i = 0; i < S::kMTiles; ++i)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) o[i][n][j] *= shrink[j & 1];
+                }
+                if (steps) {
+                    // Raw scores below the maximum's: what follows is the same for all
+                    // rows.  1 / c times c is off by 2^-23, of a difference.
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            if (!in_steps<D>(c[n][j])) continue;
+                            const float most = top[n][j] == -INFINITY ? 0.0f : top[n][j];
+                            ref[n][j] = -kShift;
+#pragma unroll
+                            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    float &x = sc[m][n][2 * h + j];
+                                    x = below_most(x, c[n][j], most) * __frcp_rn(c[n][j]);
+                                }
+                        }
                 }
             }
             uint32_t pf[2][NT][2];

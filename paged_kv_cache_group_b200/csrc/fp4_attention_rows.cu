@@ -436,11 +436,14 @@ __device__ __forceinline__ float row_max(uint32_t t_scores, int32_t from, int32_
     return fmaxf(most[0], most[1]);
 }
 
-// Their weights 2^(c s + against), written as fp16 pairs; returns the sum.
-template <bool kEdge>
+// Their weights 2^(c s - ref + kShift), written as fp16 pairs; returns the sum.
+// kSteps: unless this is false for a row, it is formed in steps, as single
+// values: the product and sum of pairs come out fused.
+template <int D, bool kEdge, bool kSteps>
 __device__ __forceinline__ float row_weights(uint32_t t_scores, uint32_t t_weights, int32_t from, int32_t to,
-                                             float c, float against) {
+                                             float c, float ref) {
     float x[2][16];
+    const float against = kShift - ref;
     const uint64_t c2 = bits_of(c, c), against2 = bits_of(against, against);
     uint64_t sum[2] = {0, 0};
     tmem_load(t_scores, x[0]);
@@ -452,7 +455,10 @@ __device__ __forceinline__ float row_weights(uint32_t t_scores, uint32_t t_weigh
         uint32_t w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const Pair p = pair_of(fma_pair(bits_of(x[q % 2][2 * i], x[q % 2][2 * i + 1]), c2, against2));
+            const Pair s = {x[q % 2][2 * i], x[q % 2][2 * i + 1]};
+            const Pair p = kSteps && in_steps<D>(c)
+                               ? Pair{below_most(s.x, c, ref) + kShift, below_most(s.y, c, ref) + kShift}
+                               : pair_of(fma_pair(bits_of(s.x, s.y), c2, against2));
             const float a = exp2_fast(p.x), b = exp2_fast(p.y);
             sum[i % 2] = add_pair(sum[i % 2], bits_of(a, b));
             w[i] = f16x2_of(a, b);
@@ -504,7 +510,7 @@ __device__ __forceinline__ Mine take_item(const Fp4Attention &a, Shared<D> &sm, 
     m.part = it.part;
     m.busy = row / 32 * 32 < it.rows && it.tiles >= 0;
     m.live = row < it.rows;
-    m.c = 1.0f;
+    m.c = 0.0f;
     if (it.tiles < 0) return m;
     const int32_t my_row = it.row0 + min(row, it.rows - 1);
     m.place = row_place(it.token0, my_row, it.head, group);
@@ -588,67 +594,93 @@ __device__ __forceinline__ void put_out(const Fp4Attention &a, const Mine &m, fl
     tmem_before();                                     // the sums have been read
 }
 
+// Where a row's scores, weights and sums lie in tensor memory.
+struct RowPlaces {
+    uint32_t scores, weights, sums;
+};
+
+// The tiles of an item.  kSteps: some row's weights are formed in steps.
+template <int D, bool kSteps>
+__device__ __forceinline__ void softmax_tiles(Shared<D> &sm, const Waits &wait, const Mine &m, const RowPlaces &t,
+                                              uint32_t &n, float &ref, float &sum) {
+    const int32_t half = threadIdx.x / 128, row = threadIdx.x % 128;
+    const uint32_t t_scores = t.scores, t_weights = t.weights, t_sums = t.sums;
+    for (int32_t j = 0; j < m.tiles; ++j, ++n) {
+        wait(sm.c.scores, n);
+        __syncwarp();
+        tmem_after();
+        // the last product is done: sums may be rescaled, weights replaced
+        bool waited = n == 0;
+        auto summed = [&]() {
+            if (!waited) wait(sm.c.summed, n - 1);
+            waited = true;
+            __syncwarp();
+            tmem_after();
+        };
+        if (!m.busy) summed();
+        if (m.busy) {
+            const int32_t base = m.begin + j * kTokens;
+            const bool edge = base + kTokens > m.all_hi || base < m.all_lo;
+            // columns this row sees, of this thread's
+            const int32_t from = m.lo - base - kColumns * half, to = max(from, m.hi - base - kColumns * half);
+            float top = edge ? row_max<true>(t_scores, from, to) : row_max<false>(t_scores, from, to);
+            top = __fmul_rn(fmaxf(top, other_half(sm.c, half, row, top)), m.c);
+            // The reference moves where a row of the warps has outgrown it.
+            if (__any_sync(0xFFFFFFFFu, kSteps ? top - ref > kSlack : top > ref + kSlack)) {
+                const float now = fmaxf(ref, top);
+                const float f = exp2_fast(ref - (now == -INFINITY ? 0.0f : now));
+                ref = now;
+                sum *= f;
+                if (j > 0) {
+                    summed();
+#pragma unroll 1
+                    for (int q = half * (D / 32); q < (half + 1) * (D / 32); ++q) {
+                        float o[16];
+                        tmem_load(t_sums + 16 * q, o);
+                        tmem_wait_load();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] *= f;
+                        tmem_store(t_sums + 16 * q, o);
+                    }
+                }
+            }
+            const float from_ref = ref == -INFINITY ? 0.0f : ref;
+            summed();
+            sum += kSteps || edge ? row_weights<D, true, kSteps>(t_scores, t_weights, from, to, m.c, from_ref)
+                                  : row_weights<D, false, false>(t_scores, t_weights, from, to, m.c, from_ref);
+            tmem_wait_store();
+        }
+        tmem_before();
+        warp_arrive(sm.c.weights);
+    }
+}
+
+// The same out of line, where it costs the usual rows nothing.
+template <int D>
+__device__ __noinline__ void softmax_tiles_apart(Shared<D> &sm, Waits wait, Mine m, RowPlaces t, uint32_t *n,
+                                                 float *ref, float *sum) {
+    uint32_t my_n = *n;
+    float my_ref = -INFINITY, my_sum = 0.0f;
+    softmax_tiles<D, true>(sm, wait, m, t, my_n, my_ref, my_sum);
+    *n = my_n, *ref = my_ref, *sum = my_sum;
+}
+
 template <int D>
 __device__ __forceinline__ void softmax_items(const Fp4Attention &a, Shared<D> &sm, const Waits &wait,
                                               uint32_t tmem, int32_t group, float k_scale, float v_scale) {
     using L = Layout<D>;
     const int32_t half = threadIdx.x / 128, row = threadIdx.x % 128, quarter = row / 32;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t t_sums = tmem + lanes + L::kSumsAt;
-    const uint32_t t_scores = tmem + lanes + kColumns * half;
-    const uint32_t t_weights = tmem + lanes + L::kWeightsAt + L::kWeightsHalf * half;
+    const RowPlaces t = {tmem + lanes + kColumns * half, tmem + lanes + L::kWeightsAt + L::kWeightsHalf * half,
+                         tmem + lanes + L::kSumsAt};
     uint32_t n = 0, items = 0;
     Mine m = take_item<D>(a, sm, wait, items, group, k_scale);
     while (m.tiles >= 0) {
         float ref = -INFINITY, sum = 0.0f;
-        for (int32_t j = 0; j < m.tiles; ++j, ++n) {
-            wait(sm.c.scores, n);
-            __syncwarp();
-            tmem_after();
-            // the last product is done: sums may be rescaled, weights replaced
-            bool waited = n == 0;
-            auto summed = [&]() {
-                if (!waited) wait(sm.c.summed, n - 1);
-                waited = true;
-                __syncwarp();
-                tmem_after();
-            };
-            if (!m.busy) summed();
-            if (m.busy) {
-                const int32_t base = m.begin + j * kTokens;
-                const bool edge = base + kTokens > m.all_hi || base < m.all_lo;
-                // columns this row sees, of this thread's
-                const int32_t from = m.lo - base - kColumns * half, to = max(from, m.hi - base - kColumns * half);
-                float top = edge ? row_max<true>(t_scores, from, to) : row_max<false>(t_scores, from, to);
-                top = fmaxf(top, other_half(sm.c, half, row, top)) * m.c;
-                // The reference moves where a row of the warps has outgrown it.
-                if (__any_sync(0xFFFFFFFFu, top > ref + kSlack)) {
-                    const float now = fmaxf(ref, top);
-                    const float f = exp2_fast(ref - (now == -INFINITY ? 0.0f : now));
-                    ref = now;
-                    sum *= f;
-                    if (j > 0) {
-                        summed();
-#pragma unroll 1
-                        for (int q = half * (D / 32); q < (half + 1) * (D / 32); ++q) {
-                            float o[16];
-                            tmem_load(t_sums + 16 * q, o);
-                            tmem_wait_load();
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] *= f;
-                            tmem_store(t_sums + 16 * q, o);
-                        }
-                    }
-                }
-                const float against = kShift - (ref == -INFINITY ? 0.0f : ref);
-                summed();
-                sum += edge ? row_weights<true>(t_scores, t_weights, from, to, m.c, against)
-                            : row_weights<false>(t_scores, t_weights, from, to, m.c, against);
-                tmem_wait_store();
-            }
-            tmem_before();
-            warp_arrive(sm.c.weights);
-        }
+        if (__any_sync(0xFFFFFFFFu, in_steps<D>(m.c)))
+            softmax_tiles_apart<D>(sm, wait, m, t, &n, &ref, &sum);
+        else
+            softmax_tiles<D, false>(sm, wait, m, t, n, ref, sum);
         // The next item's rows are put in place while this one's last product
         // runs, and its first scores are formed while these sums are put out.
         const Mine next = take_item<D>(a, sm, wait, ++items, group, k_scale);
@@ -659,7 +691,7 @@ __device__ __forceinline__ void softmax_items(const Fp4Attention &a, Shared<D> &
         }
         if (m.busy) {
             sum += other_half(sm.c, half, row, sum);
-            put_out<D>(a, m, ref, sum, t_sums, half, row, v_scale);
+            put_out<D>(a, m, ref, sum, t.sums, half, row, v_scale);
         }
         m = next;
     }
