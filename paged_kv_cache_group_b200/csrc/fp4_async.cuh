@@ -8,8 +8,8 @@
 
 namespace fp8q {
 
-constexpr int32_t kWaitTries = 1 << 20;   // polls of a barrier before giving up
-constexpr uint32_t kSleepNs = 20000;    // of one poll, at most
+constexpr int32_t kWaitTries = 1 << 23;   // polls of a barrier before giving up
+constexpr uint32_t kSleepNs = 2000;     // of one poll, at most
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -60,16 +60,42 @@ __device__ __forceinline__ void barrier_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
 }
 
-// Waits for a phase of a barrier.  Gives up after a bounded number of polls,
-// and once a block has done so, at once: its output is not valid then.
+// Waits for a phase of a barrier.  Gives up after a bounded number of polls, and
+// after one when the block already has: its output is not valid then.  Behind a
+// wait for data a warp goes on with what there is, in the rows and for the tokens
+// of its item, to the item's end; behind one for another warp's word it asks
+// told() before it uses that.  (Leaving from every wait took 1 to 3 us a call.)
 __device__ __forceinline__ void barrier_wait(uint32_t bar, uint32_t parity, volatile uint32_t *gave_up,
-                                             uint32_t *error) {
-    for (int32_t left = kWaitTries; !barrier_done(bar, parity); --left)
+                                             uint32_t *error, int32_t tries = kWaitTries) {
+    for (int32_t left = tries; !barrier_done(bar, parity); --left)
         if (left == 0 || *gave_up) {
             *gave_up = 1;
             atomicOr(error, kFp4ErrWait);
             break;
         }
+}
+
+// Whether a whole warp may use what it has waited for: no wait of the block has
+// been given up.
+__device__ __forceinline__ bool told(volatile uint32_t *gave_up) {
+    return __all_sync(0xFFFFFFFFu, *gave_up == 0);
+}
+
+// All threads of the warps that share barrier `id` meet; true if all say so.
+// Warps that meet later on leave together, or one would wait for the others.
+__device__ __forceinline__ bool agree(uint32_t id, uint32_t threads, bool ok) {
+    uint32_t all;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+                 "bar.red.and.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(all) : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(ok)) : "memory");
+    return all != 0;
+}
+
+// What a block that gave up has under way is given a while to land: two million
+// cycles, a millisecond, before it returns its shared and tensor memory.
+__device__ __forceinline__ void let_land(volatile uint32_t *gave_up) {
+    if (*gave_up)
+        for (const long long from = clock64(); clock64() - from < 2000000;) __nanosleep(1000);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {

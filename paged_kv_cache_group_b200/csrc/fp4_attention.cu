@@ -234,6 +234,7 @@ __device__ __forceinline__ void copy_items(const Fp4Attention &a, Shared<D, NT, 
 
             const uint32_t slot = items % 2;
             if (items >= 2) barrier_wait(smem_addr(&sm.item_empty[slot]), (items / 2 - 1) & 1, &sm.gave_up, &g_fp4_attention_error);
+            if (!told(&sm.gave_up)) return;
             if (lane == 0) {
                 sm.item[slot] = it;
                 if (it.part == 1) {
@@ -285,7 +286,10 @@ __device__ __forceinline__ void copy_items(const Fp4Attention &a, Shared<D, NT, 
                         stage_at<D, NT, T>(by_tile, step, m, head) + skip * S::kTile;
                     copy_async(dst, src, now.count * (by_tile ? kHeads : 1) * S::kTile, full);
                 }
-                if (++stage == S::kStages) stage = 0, ++lap;
+                if (++stage == S::kStages) {
+                    stage = 0, ++lap;
+                    if (!told(&sm.gave_up)) return;
+                }
                 now = next;
                 if (r == 0) copy_rows();
             }
@@ -295,6 +299,7 @@ __device__ __forceinline__ void copy_items(const Fp4Attention &a, Shared<D, NT, 
     }
     const uint32_t slot = items % 2;
     if (items >= 2) barrier_wait(smem_addr(&sm.item_empty[slot]), (items / 2 - 1) & 1, &sm.gave_up, &g_fp4_attention_error);
+            if (!told(&sm.gave_up)) return;
     if (lane == 0) {
         sm.item[slot].rounds = -1;
         barrier_arrive(smem_addr(&sm.item_full[slot]));
@@ -494,7 +499,7 @@ __device__ __forceinline__ void compute_items(const Fp4Attention &a, Shared<D, N
         const uint32_t slot = items % 2;
         barrier_wait(smem_addr(&sm.item_full[slot]), (items / 2) & 1, &sm.gave_up, &g_fp4_attention_error);
         const Item &it = sm.item[slot];
-        if (it.rounds < 0) return;
+        if (!(T > 1 ? agree(1, 32 * kWarps, told(&sm.gave_up)) : told(&sm.gave_up)) || it.rounds < 0) return;
 
         float c[NT][2];
         prepare_rows<D, NT, T>(a, it.rows, sm.q[slot][hh], k_scale, c);
@@ -791,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, T>::kBlocks)) fp4_atte
         copy_items<D, NT, T>(a, sm, run, d, record);
     else
         compute_items<D, NT, T>(a, sm, d, k_scale, v_scale);
-    if (*static_cast<volatile uint32_t *>(&sm.gave_up)) __nanosleep(1000000);   // copies under way land
+    let_land(&sm.gave_up);
 }
 
 // ---------------------------------------------------------------------------
@@ -895,7 +900,7 @@ __global__ void __launch_bounds__(kJoinThreads) fp4_attention_join_kernel(const 
         }
         if (i % kJoinRefill == kJoinRefill - 1 && i + 1 + kJoinSlots - kJoinRefill < s.blocks) {
             __syncthreads();                   // everybody has read the slots
-            if (threadIdx.x == 0)
+            if (threadIdx.x == 0 && *static_cast<volatile uint32_t *>(&gave_up) == 0)
                 for (int32_t k = i + 1 + kJoinSlots - kJoinRefill; k <= i + kJoinSlots && k < s.blocks; ++k) fetch(k);
         }
     }
@@ -906,7 +911,7 @@ __global__ void __launch_bounds__(kJoinThreads) fp4_attention_join_kernel(const 
             store_joined<D>(a, s, s.set * S::kHeads + hh, unit / NT, (unit % NT) * 8 + 2 * (lane % 4), x[m],
                             top[m], l[m], v_scale);
     }
-    if (*static_cast<volatile uint32_t *>(&gave_up)) __nanosleep(1000000);   // copies under way land
+    let_land(&gave_up);
 }
 
 constexpr int kFewWarps = 16;

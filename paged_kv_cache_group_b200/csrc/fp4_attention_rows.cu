@@ -210,6 +210,7 @@ __device__ __forceinline__ void walk_items(const Fp4Attention &a, Control &c, co
         if (r1 > r0) {
             const uint32_t slot = items % 2;
             if (items >= 2) wait(c.item_empty[slot], items / 2 - 1);
+            if (!told(&c.gave_up)) return;
             if (lane == 0) {
                 Item &it = c.item[slot];
                 it.begin = x.begin + r0 * kTokens;
@@ -238,6 +239,7 @@ __device__ __forceinline__ void walk_items(const Fp4Attention &a, Control &c, co
     }
     const uint32_t slot = items % 2;
     if (items >= 2) wait(c.item_empty[slot], items / 2 - 1);
+    if (!told(&c.gave_up)) return;
     if (lane == 0) {
         c.item[slot].tiles = -1;
         barrier_arrive(smem_addr(&c.item_full[slot]));
@@ -258,7 +260,7 @@ __device__ __forceinline__ void expand_items(const Fp4Attention &a, Shared<D> &s
     for (uint32_t items = 0;; ++items) {
         wait(sm.c.item_full[items % 2], items / 2);
         const Item &shared = sm.c.item[items % 2];
-        const int32_t count = shared.tiles, begin = shared.begin, first = shared.first, end = shared.end;
+        const int32_t count = told(&sm.c.gave_up) ? shared.tiles : -1, begin = shared.begin, first = shared.first, end = shared.end;
         const int32_t *table = a.block_table + static_cast<int64_t>(shared.seq) * a.table_stride;
         const int64_t head = static_cast<int64_t>(shared.head) * tiles;
         warp_arrive(sm.c.item_empty[items % 2]);
@@ -331,7 +333,7 @@ __device__ __forceinline__ void issue_items(Shared<D> &sm, const Waits &wait, ui
     uint32_t n = 0, full = 0;                  // tiles, and items with any
     for (uint32_t items = 0;; ++items) {
         wait(sm.c.item_full[items % 2], items / 2);
-        const int32_t tiles = __shfl_sync(0xFFFFFFFFu, sm.c.item[items % 2].tiles, 0);
+        const int32_t tiles = told(&sm.c.gave_up) ? __shfl_sync(0xFFFFFFFFu, sm.c.item[items % 2].tiles, 0) : -1;
         warp_arrive(sm.c.item_empty[items % 2]);
         if (tiles < 0) return;
         if (tiles == 0) continue;
@@ -495,14 +497,15 @@ struct Mine {
 };
 
 // The next item: its query rows go to shared memory once the last product with
-// the present ones is done, which the caller knows.
+// the present ones is done, which the caller knows.  None if a wait was given up.
 template <int D>
 __device__ __forceinline__ Mine take_item(const Fp4Attention &a, Shared<D> &sm, const Waits &wait, uint32_t items,
                                           int32_t group, float k_scale) {
     constexpr int kPieces = D / 16;                    // 16-byte pieces of half a query row
     const int32_t half = threadIdx.x / 128, row = threadIdx.x % 128;
     wait(sm.c.item_full[items % 2], items / 2);
-    const Item it = sm.c.item[items % 2];
+    Item it = sm.c.item[items % 2];
+    if (!agree(row / 32 + 1, 64, told(&sm.c.gave_up))) it.tiles = -1;
     warp_arrive(sm.c.item_empty[items % 2]);
     Mine m;
     m.tiles = it.tiles;
@@ -768,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D>::kBlocks) fp4_attention_ro
     __syncwarp();
     tmem_before();
     __syncthreads();
-    if (*static_cast<volatile uint32_t *>(&c.gave_up)) __nanosleep(1000000);   // products under way end
+    let_land(&c.gave_up);
     if (warp == kIssueThread / 32) {
         tmem_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "n"(L::kColumns));
