@@ -716,6 +716,7 @@ FP8Q_API int64_t fp4_kv_attention_workspace_uneven(int64_t batch, int64_t num_to
  *   inv_freq      device fp64 [rotary_dim / 2] (may be NULL with rotary_dim 0)
  *   q_weight,
  *   k_weight      device bf16 [head_dim], 16-byte aligned, or NULL: no norm
+ *                 (aligned or NULL, but not read, for a tensor without heads)
  *   num_tokens    0 .. 2^31 - 1; 0 is a no-op
  *   num_q_heads,
  *   num_kv_heads  >= 0, not both 0 and at most 65536 together; a tensor

@@ -208,11 +208,14 @@ FP8Q_API fp8q_status qk_norm_rope(const void *q, const void *k, int64_t q_stride
     const int64_t stride[2] = {q_stride, k_stride}, out_stride[2] = {q_out_stride, k_out_stride};
     const int32_t heads[2] = {num_q_heads, num_kv_heads};
     for (int i = 0; i < 2; ++i) {
-        if (heads[i] == 0) continue;
+        if (!aligned(weight[i], 16)) return FP8Q_EINVAL;
+        if (heads[i] == 0) {
+            weight[i] = nullptr;               // the kernel loads it before it counts heads
+            continue;
+        }
         const int64_t width = static_cast<int64_t>(heads[i]) * head_dim;
         if (in[i] == nullptr || out[i] == nullptr) return FP8Q_EINVAL;
-        if (!aligned(in[i], 16) || !aligned(out[i], 16) || !aligned(weight[i], 16))
-            return FP8Q_EINVAL;
+        if (!aligned(in[i], 16) || !aligned(out[i], 16)) return FP8Q_EINVAL;
         if (!valid_stride(stride[i], width) || !valid_stride(out_stride[i], width))
             return FP8Q_EINVAL;
         if (stride[i] > INT64_MAX / 4 / num_tokens || out_stride[i] > INT64_MAX / 4 / num_tokens)
@@ -232,8 +235,8 @@ FP8Q_API fp8q_status qk_norm_rope(const void *q, const void *k, int64_t q_stride
     r.k_out_stride = k_out_stride;
     r.positions = positions;
     r.inv_freq = inv_freq;
-    r.q_weight = static_cast<const uint16_t *>(q_weight);
-    r.k_weight = static_cast<const uint16_t *>(k_weight);
+    r.q_weight = static_cast<const uint16_t *>(weight[0]);
+    r.k_weight = static_cast<const uint16_t *>(weight[1]);
     r.num_tokens = num_tokens;
     r.q_heads = num_q_heads;
     r.k_heads = num_kv_heads;
