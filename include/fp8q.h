@@ -614,7 +614,8 @@ FP8Q_API fp8q_status fp4_kv_write(const void *k, const void *v, int64_t key_stri
  * of slots past the pool (FP8Q_DEVERR_SLOT_OUT_OF_RANGE).  A slot may be read
  * any number of times.
  *
- *   k, v          device bf16 rows to write, as for fp4_kv_write
+ *   k, v          device bf16 rows to write, as for fp4_kv_write; they must not
+ *                 overlap each other
  * Returns FP8Q_OK, FP8Q_EINVAL, FP8Q_ECUDA.
  */
 FP8Q_API fp8q_status fp4_kv_read(void *k, void *v, int64_t key_stride, int64_t value_stride,
@@ -711,7 +712,7 @@ FP8Q_API int64_t fp4_kv_attention_workspace_uneven(int64_t batch, int64_t num_to
  *                 q_stride and k_stride elements apart (multiples of 8)
  *   q_out, k_out  like q and k, with strides of their own; an output may be
  *                 its input (same address and stride) and must not overlap an
- *                 input otherwise
+ *                 input otherwise, nor the other output
  *   positions     device int64 [num_tokens]
  *   inv_freq      device fp64 [rotary_dim / 2] (may be NULL with rotary_dim 0)
  *   q_weight,

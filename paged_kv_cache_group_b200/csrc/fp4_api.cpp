@@ -20,6 +20,29 @@ bool valid_scale(float s) { return s >= fp8q::kFp4MinScale && s <= fp8q::kFp4Max
 // Row stride of a [rows, width] bf16 tensor.
 bool valid_stride(int64_t stride, int64_t width) { return stride >= width && stride % 8 == 0; }
 
+// Whether two [rows, width] bf16 tensors share memory; strides are valid_stride's.
+bool rows_overlap(const void *a, int64_t a_stride, int64_t a_width, const void *b, int64_t b_stride,
+                  int64_t b_width, int64_t rows) {
+    const int64_t a0 = reinterpret_cast<intptr_t>(a) / 2, b0 = reinterpret_cast<intptr_t>(b) / 2;
+    if (a0 + (rows - 1) * a_stride + a_width <= b0 || b0 + (rows - 1) * b_stride + b_width <= a0)
+        return false;
+    if (a_stride == b_stride) {
+        // Row i + k of b begins at d + k * stride of row i of a.  Only the first of
+        // them at or behind its beginning and the one before can reach into it.
+        const int64_t d = b0 - a0, behind = (d % a_stride + a_stride) % a_stride;
+        const int64_t k = (behind - d) / a_stride;
+        return (behind < a_width && k > -rows && k < rows) ||
+               (behind - a_stride + b_width > 0 && k - 1 > -rows && k - 1 < rows);
+    }
+    for (int64_t i = 0, j = 0; i < rows && j < rows;) {
+        const int64_t x = a0 + i * a_stride, y = b0 + j * b_stride;
+        if (x < y + b_width && y < x + a_width) return true;
+        if (x < y) ++i;
+        else ++j;
+    }
+    return false;
+}
+
 bool valid_dim(int32_t head_dim) { return head_dim == 64 || head_dim == 128 || head_dim == 256; }
 
 bool make_pools(void *k_pool, void *v_pool, int32_t num_kv_heads, int32_t head_dim,
@@ -117,6 +140,8 @@ FP8Q_API fp8q_status fp4_kv_read(void *k, void *v, int64_t key_stride, int64_t v
     if (!make_rows(k, v, key_stride, value_stride, slot_mapping, num_tokens, p, &r))
         return FP8Q_EINVAL;
     if (num_tokens == 0) return FP8Q_OK;
+    const int64_t width = static_cast<int64_t>(num_kv_heads) * head_dim;
+    if (rows_overlap(k, key_stride, width, v, value_stride, width, num_tokens)) return FP8Q_EINVAL;
     return from_cuda(fp8q::launch_fp4_read(r, p, static_cast<cudaStream_t>(stream)));
 }
 
@@ -162,6 +187,7 @@ FP8Q_API fp8q_status fp4_kv_attention(const void *q, int64_t q_stride, const voi
     if (num_tokens > INT64_MAX / 2 / q_stride || num_tokens > INT64_MAX / 2 / out_stride)
         return FP8Q_EINVAL;
     if (q == nullptr || out == nullptr || !aligned(q, 16) || !aligned(out, 16)) return FP8Q_EINVAL;
+    if (rows_overlap(q, q_stride, width, out, out_stride, width, num_tokens)) return FP8Q_EINVAL;
     if (seq_lens == nullptr || !aligned(seq_lens, 4) || !aligned(q_start, 4) || !aligned(lse, 4))
         return FP8Q_EINVAL;
     if ((table_width > 0 && block_table == nullptr) || !aligned(block_table, 4)) return FP8Q_EINVAL;
@@ -220,7 +246,18 @@ FP8Q_API fp8q_status qk_norm_rope(const void *q, const void *k, int64_t q_stride
             return FP8Q_EINVAL;
         if (stride[i] > INT64_MAX / 4 / num_tokens || out_stride[i] > INT64_MAX / 4 / num_tokens)
             return FP8Q_EINVAL;
-        if (in[i] == out[i] && stride[i] != out_stride[i]) return FP8Q_EINVAL;
+    }
+    for (int i = 0; i < 2; ++i) {              // an output with the inputs and the other one
+        const int64_t width = static_cast<int64_t>(heads[i]) * head_dim;
+        for (int j = 0; j < 2 && heads[i] > 0; ++j) {
+            const int64_t other = static_cast<int64_t>(heads[j]) * head_dim;
+            if (heads[j] == 0) continue;
+            if (!(i == j && in[i] == out[i] && stride[i] == out_stride[i]) &&
+                rows_overlap(out[i], out_stride[i], width, in[j], stride[j], other, num_tokens))
+                return FP8Q_EINVAL;
+            if (i < j && rows_overlap(out[i], out_stride[i], width, out[j], out_stride[j], other, num_tokens))
+                return FP8Q_EINVAL;
+        }
     }
     if (positions == nullptr || !aligned(positions, 8)) return FP8Q_EINVAL;
     if ((rotary_dim > 0 && inv_freq == nullptr) || !aligned(inv_freq, 8)) return FP8Q_EINVAL;
