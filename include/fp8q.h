@@ -22,7 +22,8 @@
  *    division of x by the scale, then rounded to E4M3 to nearest-even,
  *    saturating to +-448, keeping the sign of zero.  Results are bit-identical
  *    to a plain CPU restatement of these definitions.  Inputs must be finite
- *    (no NaN, no infinity).
+ *    (no NaN, no infinity).  Sections 4 and 5 give their own arithmetic; the
+ *    cache of section 4 is bit-identical to its restatement too.
  *  - Memory.  Every pointer except the calibration handle is DEVICE memory
  *    owned by the caller; the library allocates no device memory and frees
  *    none.  Sizes and strides are in ELEMENTS unless the name says bytes.
@@ -34,7 +35,8 @@
  *    returns FP8Q_ECUDA.  Conditions only the device can see (a slot past the
  *    end of the pool, a device-resident scale that is not a positive number)
  *    skip the affected writes and set a bit in a sticky per-device error word
- *    read by fp8q_device_error().  Nothing traps, nothing waits.
+ *    read by fp8q_device_error().  Nothing traps.  Only attention waits, for
+ *    its own copies and products, and gives up after a while.
  *  - Alignment.  bf16 buffers and staging buffers: 16-byte aligned, row
  *    strides multiples of 8 elements.  Code buffers and pools: 8-byte aligned.
  *    fp32 and int64 arrays: naturally aligned.
@@ -67,9 +69,9 @@ typedef int32_t fp8q_status;
 
 /* Bits of the sticky per-device error word. */
 #define FP8Q_DEVERR_SLOT_OUT_OF_RANGE 0x1u  /* slot >= num_blocks*block_size: token skipped */
-#define FP8Q_DEVERR_BAD_SCALE 0x2u          /* device scale NaN or <= 0: tensor not written */
+#define FP8Q_DEVERR_BAD_SCALE 0x2u          /* device scale NaN or <= 0 (4-bit cache: outside its range): tensor not written */
 #define FP8Q_DEVERR_BAD_SEQUENCE 0x4u       /* sequence length or query range outside its buffers: cut */
-#define FP8Q_DEVERR_WAIT 0x8u               /* a copy did not arrive in time: output not valid */
+#define FP8Q_DEVERR_WAIT 0x8u               /* a copy or product of attention did not end in time: output not valid */
 
 /* E4M3 saturation value and the group width of the activation quantizer. */
 #define FP8Q_E4M3_MAX 448.0f
@@ -572,6 +574,14 @@ FP8Q_API int32_t fp8_kv_graphs_ready(const int8_t *states, int64_t n);
  *                 aligned; a value outside that range sets
  *                 FP8Q_DEVERR_BAD_SCALE and its tensor (for attention: every
  *                 output) is left unwritten
+ *
+ * Which scales.  A block whose largest magnitude lies in [6 * 2^-6 s, 2688 s]
+ * has a normal block scale under the tensor's scale s, and each of its values is
+ * kept to within 0.178 of that magnitude.  The scales that a calibrator freezes
+ * (section 3: s = amax * headroom / 448) do as they are: the calibrated maximum's
+ * block scale is 75 / headroom, blocks down to 1/4779 of amax * headroom are
+ * normal, and values up to 6 * headroom times amax are held.  All tokens of a
+ * pool are read with one pair of scales: freeze before the first write.
  */
 
 /*
@@ -639,7 +649,8 @@ FP8Q_API fp8q_status fp4_kv_read(void *k, void *v, int64_t key_stride, int64_t v
  * A row that sees no token gets out = 0 and lse = -infinity.  Rows of q that no
  * sequence has keep what out and lse held.  Scores, sums and outputs are fp32,
  * rounded once to bf16; the softmax weights are rounded to fp16 for the second
- * product.  A NaN in a query row reaches that row's outputs alone.  The result
+ * product, and a query row is held in fp16 times a power of two of its own, which
+ * is exact but for elements below 2^-22 of its largest.  A NaN in a query row reaches that row's outputs alone.  The result
  * does not depend on what unused slots hold, and is the same in every run on one
  * kind of GPU.
  *
