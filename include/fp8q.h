@@ -655,7 +655,9 @@ FP8Q_API fp8q_status fp4_kv_read(void *k, void *v, int64_t key_stride, int64_t v
  * kind of GPU.
  *
  * The lengths and tables are read on the device, and the launches depend on
- * the sizes alone: a captured call may be replayed with other contents.  A
+ * the sizes alone: a captured call may be replayed with other contents.  The
+ * kernel goes by num_tokens / batch, rows that no sequence has included: pieces of
+ * prompts and single tokens are right in one call and faster in two.  A
  * length below 0 or past the table and a query range outside the rows are cut
  * to what is there (FP8Q_DEVERR_BAD_SEQUENCE); for a block outside the pool
  * block 0 is read (FP8Q_DEVERR_SLOT_OUT_OF_RANGE).  Entries of block_table

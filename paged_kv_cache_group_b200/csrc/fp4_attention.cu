@@ -41,10 +41,11 @@
 // over lanes only when some lane sees a larger score.
 //
 // Measured, 256 sequences of 3001-6000 tokens x 4 heads of 128 (664 MB):
-// 132 us with the join, 5.0 TB/s; the kernel alone 126, of which its copies
-// alone would take 109 and its arithmetic alone 107 (158 us with a copy for
-// each head).  One sequence of 200003 tokens 38 us, of which 9000 cycles pass
-// before the first product and 6 us in the join.
+// 137 us with the join in a graph, 4.8 TB/s, and 155 in separate calls; of the
+// kernel alone its copies would take 109 and its arithmetic 107 (158 us with a
+// copy for each head).  One sequence of 200003 tokens 40 us, of which 9000 cycles
+// pass before the first product and 6 us in the join.  The checks of large scores
+// and of waits that gave up are 0.4 to 1.9 us of these and of the times below.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -779,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, T>::kBlocks)) fp4_atte
         barrier_init(smem_addr(&sm.item_empty[threadIdx.x]), kWarps);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    pdl_wait();
+    pdl_wait();                                // nothing to wait for: not launched early
     pdl_allow_next();
 
     float k_scale, v_scale;
@@ -1054,11 +1055,15 @@ constexpr int64_t kFewFours = 32;
 
 // Warps of a head: a block takes as many of two heads as divide their number,
 // and four where the blocks' runs can be long.  Four heads in one copy read
-// faster, and leave twice the parts to join.  Measured with 4 heads of 128 and
-// 3000-6000 tokens, four heads against two: 48 sequences (20 steps of a block)
-// 38.9 and 38.2 us, 96 (41) 61.2 and 61.5, 160 (68) 88.9 and 93.2; 64 of 1-8192
-// (37 if all were as long as the longest) 30.0 and 26.9; with rows for two
-// tiles, 32 drafts (37) 36.7 and 39.5.
+// faster, and leave twice the parts to join.  The lengths are on the device, so
+// the table's width stands for them: steps of a block are counted as if every
+// sequence filled its table, and a table padded to the longest context takes four
+// heads from 32 sequences on.  Measured with 4 heads of 128, four heads against
+// two: 48 sequences of 3000-6000 tokens (20 steps of a block) 41.2 and 40.4 us, 64
+// (27) 47.9 and 49.4, 96 (41) 60.6 and 63.9, 160 (68) 88.7 and 95.1; spread over
+// 1-8192 tokens, where the parts count for more, 64 (35) 30.8 and 26.7, 96 (53)
+// 31.8 and 30.0, 128 (71) 31.2 and 29.4; with rows for two tiles, 8 heads and
+// 100-4000 tokens, 16 drafts (19) 39.4 and 39.4, 32 (38) 52.5 and 55.5.
 int warps_of_head(const Fp4Attention &a, int32_t rows) {
     const int32_t heads = a.pools.heads;
     const int64_t fours = fours_of(a.batch, a.num_tokens, a.q_heads / heads, heads, rows);
@@ -1124,9 +1129,13 @@ cudaError_t launch_heads(const Fp4Attention &a, cudaStream_t stream) {
 
 // More than 32 rows a sequence on average: their tiles are shared.  Measured
 // with 32 sequences of 1000-3000 tokens and 8 heads of 64 and 128, this kernel
-// against the one by rows: 30 rows 39 and 54 us against 46 and 65; 35 rows
-// (three tiles) 51 and 72 against 49 and 69; 60 rows 60 and 95 against 51 and
-// 73.  With 256, 30 rows 117 against 145, 40 rows 150 against 147.
+// against the one by rows: 30 rows 42 and 61 us against 53 and 72; 35 rows
+// (three tiles) 55 and 83 against 56 and 77; 60 rows 62 and 100 against 54 and
+// 75.  With 256, 30 rows 201 and 330 against 329 and 462, 40 rows 300 and 489
+// against 365 and 500.  The average is all that sizes tell: in a call of pieces of
+// prompts and single tokens each is in the other's kernel.  64 single tokens on
+// 3000-6000 and a piece of 512 on 4096 (4 heads of 128, 8 rows a token) take 182 us
+// together, 47 and 75 in calls of their own.
 bool fp4_attention_by_rows(int64_t batch, int64_t num_tokens, int32_t group) {
     return num_tokens * group > 32 * batch;
 }

@@ -22,7 +22,7 @@
 // each, which is why a row has two threads.
 //
 // Measured, 4 pieces of 200-500 tokens x 48 heads of 64 on 2000-4001 cached
-// tokens with a window of 1024 (14.4 GFLOP): 59 us, 242 TFLOP/s; 105 us with
+// tokens with a window of 1024 (14.4 GFLOP): 60 us, 240 TFLOP/s; 105 us with
 // the kernel for few rows.
 //
 // Operands are exact as there: code * block scale in fp16, and a query row
@@ -739,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D>::kBlocks) fp4_attention_ro
         barrier_init(smem_addr(&c.summed), 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    pdl_wait();
+    pdl_wait();                                // nothing to wait for: not launched early
     pdl_allow_next();
 
     float k_scale, v_scale;
