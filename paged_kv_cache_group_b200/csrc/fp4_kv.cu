@@ -19,7 +19,7 @@
 //
 // Measured: 60001 tokens x 8 heads of 64 read in 30.7 us (5.1 TB/s, 40.5 with
 // one token a warp); 4593 tokens x 4 heads of 128 written and read back in 9.4
-// to 10.4 us, by box, for 24 MB: two launches that are mostly latency.
+// to 10.4 us, by GPU, for 24 MB: two launches that are mostly latency.
 #include <cuda_runtime.h>
 
 #include "fp4_device.cuh"
